@@ -57,7 +57,10 @@ extern "C" {
 #define GPT_DEVERR_TARGET  2u   /* target id outside [-1, vocab)              */
 #define GPT_DEVERR_SEGMENT 4u   /* seg_ids decrease inside a row              */
 #define GPT_DEVERR_TIMEOUT 8u   /* a bounded wait in a kernel gave up         */
-#define GPT_DEVERR_POS     16u  /* position beyond max_seq (decode)           */
+#define GPT_DEVERR_POS     16u  /* position beyond max_seq (decode), or
+                                   outside a cache row's pages               */
+#define GPT_DEVERR_PAGE    32u  /* page or row id out of range, or no free page */
+#define GPT_DEVERR_START   64u  /* row starts decrease or leave [0, rows]    */
 
 /*
  * Model shape and numerics.  Architecture: token embedding plus a learned
@@ -400,6 +403,147 @@ int gpt_gemm_bf16_splitk_noalloc(int M, int N, int K, const void* A, long lda, i
  * device wait give up (its C holds NaN), else GPT_OK, and clears the word.
  * Allocates nothing.  Errors: GPT_ERR_CUDA. */
 int gpt_noalloc_status(void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Key/value cache held in 8 bits, in pages ("NTransformer" page: a KV cache
+ * and grouped-query attention on a GPU whose memory is the limit).  The calls
+ * below need no model: the caller owns the memory, and every call enqueues on
+ * `stream` (a cudaStream_t; NULL = legacy default) of the current device,
+ * allocates nothing and never waits for the device, so all can be captured
+ * into a CUDA graph.  GPT_ERR_ARG comes with the reason in
+ * gpt_last_error(NULL).  gpt_sample_parallel runs a model's decoding on them.
+ *
+ * A page holds `page` consecutive tokens of one sequence for every key/value
+ * head of every layer, and each (layer, page, head) has one fp32 scale for its
+ * keys and one for its values: a stored value is code * scale.
+ *  kind       GPT_KV8_INT8 (codes -127..127) or GPT_KV8_E4M3 (the 8-bit float
+ *             with 4 exponent and 3 fraction bits, largest value 448)
+ *  head_dim   16, 32, 64 or 128;  page  16, 32, 64 or 128 tokens
+ *  k          device [n_layers][n_pages][n_kv_heads][page][head_dim] bytes
+ *  v          device [n_layers][n_pages][n_kv_heads][page/16][head_dim][16]
+ *             bytes: 16 tokens of a channel lie together, so that the product
+ *             of weights and values reads 16 consecutive bytes per channel
+ *  k_scale, v_scale  device float [n_layers][n_pages][n_kv_heads]
+ * k and v are 16-byte aligned. */
+#define GPT_KV8_INT8 0
+#define GPT_KV8_E4M3 1
+typedef struct {
+  int32_t kind, n_layers, n_pages, n_kv_heads, head_dim, page;
+  void *k, *v;
+  float *k_scale, *v_scale;
+} gpt_kv8_cache;
+
+/* The sequences of one call.  Sequence b owns the rows start[b] ..
+ * start[b + 1] - 1 of the call's matrices (queries, keys, values, outputs):
+ * its newest tokens, the last of them at position lens[b] - 1, so lens[b]
+ * counts the tokens of the call too.  Token t lies in slot t % page of page
+ * table[b * ld_table + t / page].
+ *  start   device int32 [B + 1], non-decreasing, within [0, rows]; NULL: one
+ *          row each (rows = B).  Rows outside [start[0], start[B]) are left
+ *          as they are.
+ *  lens    device int32 [B]
+ *  table   device int32 [B][ld_table], at most max_pages entries of a row used
+ *  rows    rows of the matrices
+ * What the device finds wrong is recorded in the device word *err (GPT_DEVERR_*
+ * bits ORed in; err may be NULL) and costs no access outside the buffers:
+ * tokens at positions below 0 or beyond max_pages * page are skipped (POS), and
+ * so are the tokens of a page id outside [0, n_pages) (PAGE). */
+typedef struct {
+  const int32_t *start, *lens, *table;
+  int32_t B, max_pages, ld_table, rows;
+} gpt_kv8_batch;
+
+/* Quantise new keys and values (16-bit, dtype GPT_PRECISION_BF16 or _FP16) into
+ * the pages of their sequences, in one layer.  Row r holds head h's values at
+ * k[r * ldk + h * head_dim].  Per (page, head): with a the largest magnitude
+ * among the call's tokens in the page, the scale becomes the larger of
+ * a / 127 (int8; a / 448 for e4m3) and the present scale, if the page holds
+ * earlier tokens of the sequence, whose codes are rounded anew when the scale
+ * grows; codes are rounded to the nearest, half to even.  A scale below the
+ * smallest normal fp32 becomes 0 (all codes 0); with an infinity or a NaN among
+ * the values it becomes NaN, and so does what is read of that page and head.
+ * Slots behind the sequence's end hold unspecified codes.
+ * ldk and ldv are multiples of 8, k and v 16-byte aligned.  A page that is
+ * written must belong to one sequence of the call only (see gpt_kv8_fork).
+ * Errors: GPT_ERR_ARG, GPT_ERR_CUDA. */
+int gpt_kv8_append(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, const void* k, long ldk, const void* v,
+                   long ldv, int dtype, uint32_t* err, void* stream);
+
+/* The cached keys and values of the sequences' last tokens in 16 bits (code *
+ * scale, rounded once): rows as in gpt_kv8_append.  Skipped tokens give 0. */
+int gpt_kv8_read(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, void* k, long ldk, void* v, long ldv,
+                 int dtype, uint32_t* err, void* stream);
+
+/* Softmax attention of the sequences' newest queries over their cache in one
+ * layer: for query head h of a row at position t, out = sum_s w_s v_s with
+ * w = softmax(scale * q . k_s) over the tokens s <= t of key/value head
+ * h / (n_heads / n_kv_heads); lse = log sum_s exp(scale * q . k_s).  A row that
+ * sees no token gives out = 0, lse = -inf; a query with an infinity or a NaN
+ * gives NaN.  The call's own tokens are read from the cache, so gpt_kv8_append
+ * comes first.
+ *  q, out  device [rows], 16-bit (dtype as above), head h at r * ldq + h *
+ *          head_dim (r * ldo + ...); ldq, ldo multiples of 8, 16-byte aligned
+ *  lse     device float [rows][n_heads], or NULL
+ *  work    device scratch of gpt_kv8_attention_work bytes, 16-byte aligned;
+ *          its contents need not survive or be set.  Calls that may run at the
+ *          same time need one each.
+ * Products are summed in fp32; the softmax weights are rounded to fp16 for
+ * their product with the codes.  The same call gives the same bits.
+ * Errors: GPT_ERR_ARG (also: n_heads no multiple of n_kv_heads, work_bytes too
+ * small, scale not finite), GPT_ERR_CUDA. */
+int gpt_kv8_attention(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, const void* q, long ldq, int n_heads,
+                      int dtype, float scale, void* out, long ldo, float* lse, void* work, size_t work_bytes,
+                      uint32_t* err, void* stream);
+/* Bytes of scratch that gpt_kv8_attention needs for a batch with this B, rows
+ * and max_pages (its pointers are not read), on the current device. */
+int gpt_kv8_attention_work(const gpt_kv8_cache* c, const gpt_kv8_batch* b, int n_heads, size_t* bytes);
+
+/* Which pages the rows (sequences) of a cache hold, kept on the device.
+ *  table  device int32 [n_rows][ld_table]: entries 0 .. ceil(lens/page) - 1 of
+ *         a row are its pages; the others are never read, and -1 once freed
+ *  lens   device int32 [n_rows]: tokens of each row (0: empty)
+ *  ref    device int32 [n_pages]: rows that hold the page (0: free)
+ * All zero lens and refs is an empty pool.  n_rows <= 16384. */
+typedef struct {
+  int32_t *table, *lens, *ref;
+  int32_t n_rows, max_pages, ld_table, n_pages, page;
+} gpt_kv8_pool;
+
+/* Grow every row r by add[r] >= 0 tokens (device int32 [n_rows]): the pages it
+ * lacks for them are taken from the pool, in the order of rows and of their
+ * pages the lowest free ones first, and lens[r] += add[r].  A row with a negative
+ * add or whose length would pass max_pages * page stays as it was (POS).  From
+ * the first row on whose pages the pool cannot provide, the rows that need
+ * pages stay as they were (PAGE).
+ * The tokens themselves are written by gpt_kv8_append. */
+int gpt_kv8_extend(const gpt_kv8_pool* p, const int32_t* add, uint32_t* err, void* stream);
+
+/* For i in 0..n-1 (device int32 src[n], dst[n]): row dst[i], empty before,
+ * becomes a copy of row src[i].  Full pages are shared (ref + 1); a last page
+ * that is only partly filled is copied in every layer to the lowest free page
+ * (the copies in the order of i), so that both rows can be appended to.  All
+ * sources are taken as they were before the call.  Of several i with the same
+ * dst the first one counts.
+ *  done  device int32 [n]: 1 where the fork was made; 0 where src or dst is out
+ *        of range, dst was not empty, an earlier i has the same dst, or no free
+ *        page was left (for this one or an earlier one); *err gets PAGE
+ * n <= 16384.  c must have the pool's n_pages and page. */
+int gpt_kv8_fork(const gpt_kv8_pool* p, const gpt_kv8_cache* c, const int32_t* src, const int32_t* dst, int n,
+                 int32_t* done, uint32_t* err, void* stream);
+
+/* Empty n rows (device int32 rows[n]; a row listed twice is freed once): the
+ * references to their pages are dropped, their table entries become -1 and
+ * their lens 0.  A page without references is free. */
+int gpt_kv8_free(const gpt_kv8_pool* p, const int32_t* rows, int n, uint32_t* err, void* stream);
+
+/* Move pages so that the pages in use are 0 .. n_live - 1: the k-th lowest free
+ * page below n_live gets the k-th lowest used one from n_live on, with its codes
+ * and scales in every layer, and the table and ref follow.  Pages below n_live
+ * that are in use stay.
+ *  n_live  device int32 [1], or NULL
+ *  work    device int32 [2 * n_pages + 8], contents irrelevant */
+int gpt_kv8_compact(const gpt_kv8_pool* p, const gpt_kv8_cache* c, int32_t* n_live, int32_t* work, uint32_t* err,
+                    void* stream);
 
 /* Number of kernels libgpt has launched in this process (all handles).
  * Benchmarks read it before and after a timed region. */

@@ -16,6 +16,8 @@ typedef __half f16;
 #define GPT_DEVERR_SEGMENT 4u
 #define GPT_DEVERR_TIMEOUT 8u
 #define GPT_DEVERR_POS 16u
+#define GPT_DEVERR_PAGE 32u
+#define GPT_DEVERR_START 64u
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }

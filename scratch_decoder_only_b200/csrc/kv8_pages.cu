@@ -1,0 +1,498 @@
+// The pages of the 8-bit key/value cache: growing rows, forking, freeing and
+// compacting them, all decided on the device (include/gpt.h).
+//
+// Free pages are the zeros of ref[n_pages]; a request takes the k-th lowest
+// one.  One cluster of eight blocks reads ref twice, each block a slice: first
+// it counts the zeros, the counts meet in distributed shared memory, then it
+// ranks them and hands page number k to the request of that rank, found by
+// bisection in the requests' running sums.  Every launch reads the whole of
+// ref (4 bytes a page; a pool of 100,000 pages is 0.4 MB in L2) and nothing
+// depends on an earlier call, so any table that a host writes is as good as one
+// that these kernels made.  What bounds them is latency: the launch, the
+// barriers between the phases and the two trips to memory, not the bytes.
+#include <cooperative_groups.h>
+#include <string>
+#include "kv8.cuh"
+
+namespace cg = cooperative_groups;
+
+#define KVP_CTAS 8
+#define KVP_THREADS 1024
+#define KVP_MAX 16384   // requests a call
+
+struct Kv8PoolP {
+  int *table, *lens, *ref;
+  int n_rows, max_pages, ld_table, n_pages, lp;
+  unsigned* err;
+};
+
+// Exclusive sum over the block in thread order; total: of the whole block.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, k);
+    if (lane >= k) inc += y;
+  }
+  __syncthreads();   // the sums of an earlier call have been read
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int w = warp_sums[lane];
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, k);
+    if (lane >= k) w += y;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+  return (warp ? before : 0) + inc - v;
+}
+
+// This block's slice of the pages, and four pages of it: bit i of the result
+// is set where page i0 + i is in the slice and (live) in use or (!live) free.
+struct Slice {
+  int a, b;
+};
+__device__ __forceinline__ Slice kvp_slice(int n, int rank) {
+  const int per = ((n + KVP_CTAS - 1) / KVP_CTAS + 3) & ~3;
+  return {min(n, rank * per), min(n, (rank + 1) * per)};
+}
+__device__ __forceinline__ unsigned kvp_mask(const int* ref, int i0, int end, bool live) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i0 + i < end && (ref[i0 + i] > 0) == live) m |= 1u << i;
+  return m;
+}
+
+// Each block's value v, as the sum over the blocks before this one and over all.
+__device__ __forceinline__ int cluster_sum(cg::cluster_group& cl, int* slot, int v, int& total) {
+  if (threadIdx.x == 0) *slot = v;
+  cl.sync();
+  int before = 0, all = 0;
+  for (int r = 0; r < KVP_CTAS; ++r) {
+    const int x = *cl.map_shared_rank(slot, r);
+    before += r < (int)cl.block_rank() ? x : 0;
+    all += x;
+  }
+  total = all;
+  return before;
+}
+
+// FORK = false: request i grows row i by add[i].  FORK = true: request i makes
+// row dst[i] a copy of row src[i].  Both need pages; fork's copies of them
+// follow in kvp_copy_kernel.
+//
+// Forks to the same row: the claims are negative numbers put into lens[dst]
+// (0 while empty) with a minimum, so the first pair wins whatever the order of
+// the threads; the row's length replaces the claim at the end.
+template <bool FORK>
+__global__ void __cluster_dims__(KVP_CTAS, 1, 1) __launch_bounds__(KVP_THREADS)
+    kvp_grow_kernel(Kv8PoolP p, const int* __restrict__ add, const int* __restrict__ src, const int* __restrict__ dst,
+                    int n, int* __restrict__ done) {
+  griddep_wait();
+  griddep_release();
+  extern __shared__ int first[];   // [n + 1] running sum of the pages needed
+  __shared__ int wsum[32], slot, sflag;
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = cl.block_rank(), tid = threadIdx.x;
+  const int P1 = (1 << p.lp) - 1, claim0 = -0x7fffffff;
+  if (FORK) {
+    if (rank == 0) {
+      for (int i = tid; i < n; i += KVP_THREADS) {
+        const int a = src[i], z = dst[i];
+        first[i] = (unsigned)a < (unsigned)p.n_rows && (unsigned)z < (unsigned)p.n_rows && p.lens[z] == 0;
+      }
+      __syncthreads();
+      for (int i = tid; i < n; i += KVP_THREADS)
+        if (first[i]) atomicMin(&p.lens[dst[i]], claim0 + i);
+      __threadfence();
+    }
+    cl.sync();
+  }
+  // ---- pages that each request needs (an invalid one: none)
+  int carry = 0;
+  bool bad_pos = false;
+  for (int i0 = 0; i0 < n; i0 += KVP_THREADS) {
+    const int i = i0 + tid;
+    int need = 0;
+    if (i < n) {
+      if (FORK) {
+        const int z = dst[i], a = src[i];
+        if ((unsigned)z < (unsigned)p.n_rows && (unsigned)a < (unsigned)p.n_rows && p.lens[z] == claim0 + i) {
+          const int len = p.lens[a];
+          need = len > 0 && (len & P1) && ((len - 1) >> p.lp) < p.max_pages;
+        }
+      } else {
+        const int len = p.lens[i], ad = add[i];
+        const long want = (long)len + ad;
+        if (ad < 0 || len < 0 || want > ((long)p.max_pages << p.lp)) bad_pos = true;
+        else need = (int)((want + P1) >> p.lp) - ((len + P1) >> p.lp);
+      }
+    }
+    int tot;
+    const int ex = block_scan(need, wsum, tot);
+    if (i < n) first[i] = carry + ex;
+    carry += tot;
+  }
+  if (tid == 0) first[n] = carry;
+  if (bad_pos && rank == 0) set_dev_err(p.err, GPT_DEVERR_POS);
+  __syncthreads();
+  const int total = carry;
+
+  // ---- free pages of the slice, and of the slices before
+  int avail = 0x7fffffff;
+  if (total > 0) {
+    const Slice sl = kvp_slice(p.n_pages, rank);
+    int cnt = 0;
+    for (int i = sl.a + 4 * tid; i < sl.b; i += 4 * KVP_THREADS) cnt += __popc(kvp_mask(p.ref, i, sl.b, false));
+    int mine;
+    block_scan(cnt, wsum, mine);
+    int base = cluster_sum(cl, &slot, mine, avail);
+    // ---- rank them; page number k of the pool goes to the request that holds rank k
+    for (int i0 = sl.a; i0 < sl.b && base < total; i0 += 4 * KVP_THREADS) {
+      const int i = i0 + 4 * tid;
+      unsigned m = i < sl.b ? kvp_mask(p.ref, i, sl.b, false) : 0u;
+      int tot;
+      int k = base + block_scan(__popc(m), wsum, tot);
+      for (; m && k < total; m &= m - 1, ++k) {
+        const int id = i + __ffs(m) - 1;
+        int lo = 0, hi = n - 1;   // the last request with first <= k
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (first[mid] <= k) lo = mid;
+          else hi = mid - 1;
+        }
+        if (first[lo + 1] > avail) break;   // not served: no later rank is either
+        const int r = FORK ? dst[lo] : lo;
+        const int len = FORK ? p.lens[src[lo]] : p.lens[lo];
+        const int at = (FORK ? len >> p.lp : (len + P1) >> p.lp) + k - first[lo];
+        p.table[(long)r * p.ld_table + at] = id;
+        p.ref[id] = 1;
+      }
+      base += tot;
+    }
+  }
+  // ---- whole pages of the forks: shared
+  if (FORK) {
+    const int warps = KVP_CTAS * (KVP_THREADS / 32), w = rank * (KVP_THREADS / 32) + (tid >> 5), lane = tid & 31;
+    for (int i = w; i < n; i += warps) {
+      const int a = src[i], z = dst[i];
+      if ((unsigned)a >= (unsigned)p.n_rows || (unsigned)z >= (unsigned)p.n_rows || p.lens[z] != claim0 + i) continue;
+      if (first[i + 1] > first[i] && first[i + 1] > avail) continue;
+      const int full = min(max(p.lens[a], 0) >> p.lp, p.max_pages);
+      for (int j = lane; j < full; j += 32) {
+        const int id = p.table[(long)a * p.ld_table + j];
+        p.table[(long)z * p.ld_table + j] = id;
+        if ((unsigned)id < (unsigned)p.n_pages) atomicAdd(&p.ref[id], 1);
+        else set_dev_err(p.err, GPT_DEVERR_PAGE);
+      }
+    }
+  }
+  cl.sync();   // every block has read the lengths
+  if (rank) return;
+  // ---- the new lengths
+  if (tid == 0) sflag = 0;
+  __syncthreads();
+  if (FORK) {
+    // every fork's length first (a source that is another fork's target counts
+    // as empty: its claim is negative), then the claims are replaced
+    for (int i = tid; i < n; i += KVP_THREADS) {
+      const int a = src[i], z = dst[i];
+      int len = -1;
+      if ((unsigned)a < (unsigned)p.n_rows && (unsigned)z < (unsigned)p.n_rows && p.lens[z] == claim0 + i) {
+        len = max(p.lens[a], 0);
+        if (first[i + 1] > first[i] && first[i + 1] > avail) len = -2;   // no page for it: the row is empty again
+      }
+      if (len < 0) sflag = 1;
+      done[i] = len;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += KVP_THREADS) {
+      const int len = done[i];
+      if (len >= 0) p.lens[dst[i]] = len;
+      else if (len == -2) p.lens[dst[i]] = 0;
+      done[i] = len >= 0;
+    }
+  } else {
+    for (int i = tid; i < n; i += KVP_THREADS) {
+      const int ad = add[i], len = p.lens[i], need = first[i + 1] - first[i];
+      if (ad < 0 || len < 0 || (long)len + ad > ((long)p.max_pages << p.lp)) continue;
+      if (need && first[i + 1] > avail) sflag = 1;
+      else p.lens[i] = len + ad;
+    }
+    __syncthreads();
+  }
+  if (tid == 0 && sflag) set_dev_err(p.err, GPT_DEVERR_PAGE);
+}
+
+// ---- copies of whole pages, all layers
+struct Kv8CopyP {
+  uint8_t *k, *v;
+  float *ks, *vs;
+  long layer_pages;    // n_pages
+  int layers, Hkv;
+  int bytes;           // of one page in one layer (all heads), a multiple of 256
+};
+#define KVP_CHUNK 16384   // bytes a block copies: 256 threads x 4 vectors of 16
+
+// One chunk of one layer's keys or values of a page (sub = ((layer * 2 + is_v) *
+// chunks + chunk)); the first chunk takes the scales along.  Four 16-byte
+// loads are in flight per thread, so that a few blocks per SM cover HBM's latency.
+__device__ __forceinline__ void kvp_copy_chunk(const Kv8CopyP& c, int a, int z, int sub, int chunks) {
+  const int chunk = sub % chunks, lv = sub / chunks, layer = lv >> 1;
+  const bool is_v = lv & 1;
+  const long pa = (long)layer * c.layer_pages + a, pz = (long)layer * c.layer_pages + z;
+  uint8_t* x = is_v ? c.v : c.k;
+  const uint4* from = reinterpret_cast<const uint4*>(x + pa * c.bytes + (long)chunk * KVP_CHUNK);
+  uint4* to = reinterpret_cast<uint4*>(x + pz * c.bytes + (long)chunk * KVP_CHUNK);
+  const int n = min(c.bytes - chunk * KVP_CHUNK, KVP_CHUNK) / 16;
+  uint4 r[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (threadIdx.x + 256 * j < n) r[j] = from[threadIdx.x + 256 * j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (threadIdx.x + 256 * j < n) to[threadIdx.x + 256 * j] = r[j];
+  if (chunk == 0) {
+    float* s = is_v ? c.vs : c.ks;
+    for (int h = threadIdx.x; h < c.Hkv; h += 256) s[pz * c.Hkv + h] = s[pa * c.Hkv + h];
+  }
+}
+
+// The part-filled last pages of the forks: one block per (chunk, pair).
+__global__ void __launch_bounds__(256) kvp_fork_copy_kernel(Kv8PoolP p, Kv8CopyP c, const int* __restrict__ src,
+                                                            const int* __restrict__ dst, const int* __restrict__ done,
+                                                            int chunks) {
+  griddep_wait();
+  griddep_release();
+  const int i = blockIdx.y;
+  if (!done[i]) return;
+  const int len = p.lens[dst[i]], last = len >> p.lp;
+  if (!(len & ((1 << p.lp) - 1)) || last >= p.max_pages) return;
+  const int a = p.table[(long)src[i] * p.ld_table + last], z = p.table[(long)dst[i] * p.ld_table + last];
+  if ((unsigned)a >= (unsigned)p.n_pages || (unsigned)z >= (unsigned)p.n_pages) {
+    if (threadIdx.x == 0) set_dev_err(p.err, GPT_DEVERR_PAGE);
+    return;
+  }
+  kvp_copy_chunk(c, a, z, blockIdx.x, chunks);
+}
+
+// ---- free: one block per listed row.  The exchange of the length gives the
+// row to one of the blocks that list it.
+__global__ void __launch_bounds__(128) kvp_free_kernel(Kv8PoolP p, const int* __restrict__ rows) {
+  griddep_wait();
+  griddep_release();
+  __shared__ int slen;
+  const int r = rows[blockIdx.x];
+  if ((unsigned)r >= (unsigned)p.n_rows) {
+    if (threadIdx.x == 0) set_dev_err(p.err, GPT_DEVERR_PAGE);
+    return;
+  }
+  if (threadIdx.x == 0) slen = atomicExch(&p.lens[r], 0);
+  __syncthreads();
+  const int n = min((max(slen, 0) + (1 << p.lp) - 1) >> p.lp, p.max_pages);
+  int* row = p.table + (long)r * p.ld_table;
+  for (int j = threadIdx.x; j < n; j += 128) {
+    const int id = row[j];
+    row[j] = -1;
+    if ((unsigned)id >= (unsigned)p.n_pages) set_dev_err(p.err, GPT_DEVERR_PAGE);
+    else if (atomicSub(&p.ref[id], 1) <= 0) {
+      atomicAdd(&p.ref[id], 1);   // nobody held it
+      set_dev_err(p.err, GPT_DEVERR_PAGE);
+    }
+  }
+}
+
+// ---- compaction.  work: n_live, the number of moves, then (from entry 8 on)
+// from[k], the k-th used page from n_live on, and to[k], the k-th hole below it,
+// n_pages / 2 entries each (there are no more moves than that), then the move
+// of each page.
+__global__ void __cluster_dims__(KVP_CTAS, 1, 1) __launch_bounds__(KVP_THREADS)
+    kvp_plan_kernel(Kv8PoolP p, int* __restrict__ n_live, int* __restrict__ work) {
+  griddep_wait();
+  griddep_release();
+  __shared__ int wsum[32], slot[2];
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = cl.block_rank(), tid = threadIdx.x, n = p.n_pages, half = n / 2;
+  int *from = work + 8, *to = from + half, *move = to + half;
+  const Slice sl = kvp_slice(n, rank);
+  int cnt = 0, mine, live;
+  for (int i = sl.a + 4 * tid; i < sl.b; i += 4 * KVP_THREADS) cnt += __popc(kvp_mask(p.ref, i, sl.b, true));
+  block_scan(cnt, wsum, mine);
+  const int before = cluster_sum(cl, &slot[0], mine, live);
+  // Ranks follow from the used pages before a place: hole i is number
+  // i - used(i) of the holes, mover i number used(i) - used(live) of the movers.
+  int below = 0;   // used(live)
+  cnt = 0;
+  for (int i = sl.a + 4 * tid; i < min(sl.b, live); i += 4 * KVP_THREADS)
+    cnt += __popc(kvp_mask(p.ref, i, min(sl.b, live), true));
+  block_scan(cnt, wsum, mine);
+  cluster_sum(cl, &slot[1], mine, below);
+  const int moves = live - below;
+  if (rank == 0 && tid == 0) {
+    work[0] = live;
+    work[1] = moves;
+    if (n_live) *n_live = live;
+  }
+  int base = before;
+  for (int i0 = sl.a; i0 < sl.b; i0 += 4 * KVP_THREADS) {
+    const int i = i0 + 4 * tid;
+    const unsigned m = i < sl.b ? kvp_mask(p.ref, i, sl.b, true) : 0u;
+    int tot;
+    int used = base + block_scan(__popc(m), wsum, tot);
+    for (int e = 0; e < 4 && i + e < sl.b; ++e) {
+      const int id = i + e;
+      const bool on = m >> e & 1;
+      if (id < live && !on) to[id - used] = id;
+      if (id >= live && on) {
+        from[used - below] = id;
+        move[id] = used - below;
+      }
+      used += on;
+    }
+    base += tot;
+  }
+  cl.sync();   // no block leaves while another reads its shared memory
+}
+
+// The moves: blocks first follow them in the rows' tables, then copy pages.
+__global__ void __launch_bounds__(256) kvp_move_kernel(Kv8PoolP p, Kv8CopyP c, const int* __restrict__ work,
+                                                       int chunks) {
+  griddep_wait();
+  griddep_release();
+  const int live = work[0], moves = work[1], half = p.n_pages / 2;
+  const int *from = work + 8, *to = from + half, *move = to + half;
+  for (int r = blockIdx.x; r < p.n_rows; r += gridDim.x) {
+    const int n = min((max(p.lens[r], 0) + (1 << p.lp) - 1) >> p.lp, p.max_pages);
+    int* row = p.table + (long)r * p.ld_table;
+    for (int j = threadIdx.x; j < n; j += 256) {
+      const int id = row[j];
+      if (id >= 0 && id < live) continue;
+      const int k = (unsigned)id < (unsigned)p.n_pages ? move[id] : -1;
+      if ((unsigned)k < (unsigned)moves && from[k] == id) row[j] = to[k];
+      else set_dev_err(p.err, GPT_DEVERR_PAGE);   // a page that nobody is said to hold
+    }
+  }
+  const int per = 2 * c.layers * chunks;
+  const long jobs = (long)moves * per;
+  for (long i = blockIdx.x; i < jobs; i += gridDim.x) {
+    const int k = (int)(i / per), sub = (int)(i % per);
+    const int a = from[k], z = to[k];
+    if (sub == 0 && threadIdx.x == 0) {
+      p.ref[z] = p.ref[a];
+      p.ref[a] = 0;
+    }
+    kvp_copy_chunk(c, a, z, sub, chunks);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Entry points
+// ---------------------------------------------------------------------------
+static int kvp_refuse(const char* what, const char* why) {
+  set_global_error((std::string(what) + ": " + why).c_str());
+  return GPT_ERR_ARG;
+}
+static int kvp_done(const char* what, cudaError_t e) {
+  if (e == cudaSuccess) return GPT_OK;
+  set_global_error((std::string(what) + ": " + cudaGetErrorString(e)).c_str());
+  return GPT_ERR_CUDA;
+}
+
+static const char* kvp_check(const gpt_kv8_pool* p) {
+  if (!p) return "pool is NULL";
+  if (!p->table || !p->lens || !p->ref) return "table, lens and ref must be non-NULL";
+  if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) return "page must be 16, 32, 64 or 128";
+  if (p->n_rows < 1 || p->n_rows > KVP_MAX) return "n_rows out of range [1, 16384]";
+  if (p->n_pages < 1 || p->n_pages > (1 << 30)) return "n_pages out of range";
+  if (p->max_pages < 1 || p->ld_table < p->max_pages || (long)p->max_pages * p->page > 0x7fffff00L)
+    return "need 1 <= max_pages <= ld_table and max_pages * page < 2^31";
+  return "";
+}
+static const char* kvp_check_cache(const gpt_kv8_pool* p, const gpt_kv8_cache* c) {
+  const char* why = kv8_check_cache(c);
+  if (*why) return why;
+  if (c->n_pages != p->n_pages || c->page != p->page) return "cache and pool differ in n_pages or page";
+  return "";
+}
+static Kv8PoolP kvp_pool(const gpt_kv8_pool& p, uint32_t* err) {
+  return {p.table, p.lens, p.ref, p.n_rows, p.max_pages, p.ld_table, p.n_pages, ilog2(p.page), err};
+}
+static Kv8CopyP kvp_copy(const gpt_kv8_cache& c) {
+  return {(uint8_t*)c.k, (uint8_t*)c.v, c.k_scale, c.v_scale, c.n_pages, c.n_layers, c.n_kv_heads,
+          c.n_kv_heads * c.page * c.head_dim};
+}
+
+template <bool FORK>
+static cudaError_t kvp_grow(const Kv8PoolP& p, const int* add, const int* src, const int* dst, int n, int* done,
+                            cudaStream_t s) {
+  const size_t smem = ((size_t)n + 1) * sizeof(int);
+  if (smem > 40000) {
+    const cudaError_t e = cudaFuncSetAttribute(kvp_grow_kernel<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (KVP_MAX + 1) * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
+  }
+  ++g_kernel_launches;
+  return launch_k(kvp_grow_kernel<FORK>, dim3(KVP_CTAS), dim3(KVP_THREADS), smem, s, p, add, src, dst, n, done);
+}
+
+extern "C" {
+
+int gpt_kv8_extend(const gpt_kv8_pool* p, const int32_t* add, uint32_t* err, void* stream) {
+  const char* why = kvp_check(p);
+  if (!*why && !add) why = "add is NULL";
+  if (*why) return kvp_refuse("gpt_kv8_extend", why);
+  return kvp_done("gpt_kv8_extend", kvp_grow<false>(kvp_pool(*p, err), add, nullptr, nullptr, p->n_rows, nullptr,
+                                                    (cudaStream_t)stream));
+}
+
+int gpt_kv8_fork(const gpt_kv8_pool* p, const gpt_kv8_cache* c, const int32_t* src, const int32_t* dst, int n,
+                 int32_t* done, uint32_t* err, void* stream) {
+  const char* why = kvp_check(p);
+  if (!*why) why = kvp_check_cache(p, c);
+  if (!*why && (n < 0 || n > KVP_MAX)) why = "n out of range [0, 16384]";
+  if (!*why && n && (!src || !dst || !done)) why = "src, dst and done must be non-NULL";
+  if (*why) return kvp_refuse("gpt_kv8_fork", why);
+  if (n == 0) return GPT_OK;
+  const Kv8PoolP P = kvp_pool(*p, err);
+  const Kv8CopyP C = kvp_copy(*c);
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = kvp_grow<true>(P, nullptr, src, dst, n, done, s);
+  if (e != cudaSuccess) return kvp_done("gpt_kv8_fork", e);
+  const int chunks = (C.bytes + KVP_CHUNK - 1) / KVP_CHUNK;
+  ++g_kernel_launches;
+  return kvp_done("gpt_kv8_fork", launch_k(kvp_fork_copy_kernel, dim3((unsigned)(2 * C.layers * chunks), n), dim3(256), 0, s, P,
+                                           C, src, dst, (const int*)done, chunks));
+}
+
+int gpt_kv8_free(const gpt_kv8_pool* p, const int32_t* rows, int n, uint32_t* err, void* stream) {
+  const char* why = kvp_check(p);
+  if (!*why && (n < 0 || (n && !rows))) why = "need n >= 0 and rows non-NULL";
+  if (*why) return kvp_refuse("gpt_kv8_free", why);
+  if (n == 0) return GPT_OK;
+  ++g_kernel_launches;
+  return kvp_done("gpt_kv8_free",
+                  launch_k(kvp_free_kernel, dim3(n), dim3(128), 0, (cudaStream_t)stream, kvp_pool(*p, err), rows));
+}
+
+int gpt_kv8_compact(const gpt_kv8_pool* p, const gpt_kv8_cache* c, int32_t* n_live, int32_t* work, uint32_t* err,
+                    void* stream) {
+  const char* why = kvp_check(p);
+  if (!*why) why = kvp_check_cache(p, c);
+  if (!*why && !work) why = "work is NULL";
+  if (*why) return kvp_refuse("gpt_kv8_compact", why);
+  const Kv8PoolP P = kvp_pool(*p, err);
+  const Kv8CopyP C = kvp_copy(*c);
+  cudaStream_t s = (cudaStream_t)stream;
+  ++g_kernel_launches;
+  cudaError_t e = launch_k(kvp_plan_kernel, dim3(KVP_CTAS), dim3(KVP_THREADS), 0, s, P, n_live, work);
+  if (e != cudaSuccess) return kvp_done("gpt_kv8_compact", e);
+  const int chunks = (C.bytes + KVP_CHUNK - 1) / KVP_CHUNK;
+  ++g_kernel_launches;
+  return kvp_done("gpt_kv8_compact",
+                  launch_k(kvp_move_kernel, dim3(148 * 6), dim3(256), 0, s, P, C, (const int*)work, chunks));
+}
+
+}  // extern "C"

@@ -31,6 +31,8 @@ EXPORTED = [
     "gpt_kernel_launches", "gpt_profile_enable", "gpt_profile_read", "gpt_gemm_bf16",
     "gpt_gemm_bf16_splitk_noalloc", "gpt_noalloc_status", "gpt_set_lr_schedule", "gpt_train_steps",
     "gpt_sample_decode", "gpt_backward_accumulate", "gpt_set_loss_weight", "gpt_beam_decode", "gpt_train_step",
+    "gpt_kv8_append", "gpt_kv8_read", "gpt_kv8_attention", "gpt_kv8_attention_work", "gpt_kv8_extend",
+    "gpt_kv8_fork", "gpt_kv8_free", "gpt_kv8_compact",
 ]
 
 
@@ -75,6 +77,23 @@ class gpt_lr_schedule(ctypes.Structure):
                 ("max_lr", ctypes.c_float), ("min_lr", ctypes.c_float)]
 
 
+class gpt_kv8_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("kind", "n_layers", "n_pages", "n_kv_heads", "head_dim", "page")] + \
+               [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+
+
+class gpt_kv8_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("start", "lens", "table")] + \
+               [(n, ctypes.c_int32) for n in ("B", "max_pages", "ld_table", "rows")]
+
+
+class gpt_kv8_pool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("table", "lens", "ref")] + \
+               [(n, ctypes.c_int32) for n in ("n_rows", "max_pages", "ld_table", "n_pages", "page")]
+
+
+GPT_KV8_INT8, GPT_KV8_E4M3 = 0, 1
+
 _lib = None
 
 
@@ -87,7 +106,8 @@ def load_library(path: str = LIB_PATH):
         raise RuntimeError(f"{path} is missing: build it with `python -m scratch_decoder_only_b200.build`")
     L = ctypes.CDLL(path)
     P, I, S, F, U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_uint64
-    H = ctypes.c_void_p
+    H, LG = ctypes.c_void_p, ctypes.c_long
+    KC, KB, KP = (ctypes.POINTER(x) for x in (gpt_kv8_cache, gpt_kv8_batch, gpt_kv8_pool))
     sig = {
         "gpt_create": ([ctypes.POINTER(gpt_config), U64, ctypes.POINTER(H)], I),
         "gpt_destroy": ([H], None),
@@ -119,6 +139,14 @@ def load_library(path: str = LIB_PATH):
         "gpt_beam_decode": ([H, P, I, I, I, I, P, P], I),
         "gpt_train_steps": ([H, P, P, P, I, I, I, ctypes.POINTER(gpt_adamw), P, P, P], I),
         "gpt_train_step": ([H, P, P, P, I, I, ctypes.POINTER(gpt_adamw), P, P, P], I),
+        "gpt_kv8_append": ([KC, I, KB, P, LG, P, LG, I, P, P], I),
+        "gpt_kv8_read": ([KC, I, KB, P, LG, P, LG, I, P, P], I),
+        "gpt_kv8_attention": ([KC, I, KB, P, LG, I, I, F, P, LG, P, P, S, P, P], I),
+        "gpt_kv8_attention_work": ([KC, KB, I, ctypes.POINTER(S)], I),
+        "gpt_kv8_extend": ([KP, P, P, P], I),
+        "gpt_kv8_fork": ([KP, KC, P, P, I, P, P, P], I),
+        "gpt_kv8_free": ([KP, P, I, P, P], I),
+        "gpt_kv8_compact": ([KP, KC, P, P, P, P], I),
         "gpt_profile_read": ([H, ctypes.POINTER(gpt_prof_entry), I, ctypes.POINTER(I)], I),
     }
     for n in ("params", "grads", "adam_m", "adam_v"):
