@@ -424,7 +424,10 @@ def _compact(s):
 
 def _handle(s):
     if "cache" not in s:
-        from scratch_decoder_only_b200.kv8 import KV8Batch, KV8Cache
+        from scratch_decoder_only_b200.kv8 import KV8Batch, KV8Cache, KV8Pool
+        if s["case"]["op"] == "turnover":
+            s["cache"] = KV8Pool(s["table"], s["lens"], s["ref"], s["case"]["page"])
+            return s["cache"]
         s["cache"] = KV8Cache(s["k"], s["v"], s["k_scale"], s["v_scale"], s["table"], s["lens"], s.get("ref"))
         if "rows" in s:
             s["batch"] = KV8Batch(s["table"], s["lens"], s["start"], s["rows"])
