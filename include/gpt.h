@@ -540,9 +540,9 @@ int gpt_kv8_free(const gpt_kv8_pool* p, const int32_t* rows, int n, uint32_t* er
  * page below n_live gets the k-th lowest used one from n_live on, with its codes
  * and scales in every layer, and the table and ref follow.  Pages below n_live
  * that are in use stay.
- *  n_live  device int32 [1], or NULL
+ *  n_live  device int64 [1], or NULL
  *  work    device int32 [2 * n_pages + 8], contents irrelevant */
-int gpt_kv8_compact(const gpt_kv8_pool* p, const gpt_kv8_cache* c, int32_t* n_live, int32_t* work, uint32_t* err,
+int gpt_kv8_compact(const gpt_kv8_pool* p, const gpt_kv8_cache* c, int64_t* n_live, int32_t* work, uint32_t* err,
                     void* stream);
 
 /* Number of kernels libgpt has launched in this process (all handles).

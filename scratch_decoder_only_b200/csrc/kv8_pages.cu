@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(128) kvp_free_kernel(Kv8PoolP p, const int* __
 // n_pages / 2 entries each (there are no more moves than that), then the move
 // of each page.
 __global__ void __cluster_dims__(KVP_CTAS, 1, 1) __launch_bounds__(KVP_THREADS)
-    kvp_plan_kernel(Kv8PoolP p, int* __restrict__ n_live, int* __restrict__ work) {
+    kvp_plan_kernel(Kv8PoolP p, int64_t* __restrict__ n_live, int* __restrict__ work) {
   griddep_wait();
   griddep_release();
   __shared__ int wsum[32], slot[2];
@@ -477,11 +477,12 @@ int gpt_kv8_free(const gpt_kv8_pool* p, const int32_t* rows, int n, uint32_t* er
                   launch_k(kvp_free_kernel, dim3(n), dim3(128), 0, (cudaStream_t)stream, kvp_pool(*p, err), rows));
 }
 
-int gpt_kv8_compact(const gpt_kv8_pool* p, const gpt_kv8_cache* c, int32_t* n_live, int32_t* work, uint32_t* err,
+int gpt_kv8_compact(const gpt_kv8_pool* p, const gpt_kv8_cache* c, int64_t* n_live, int32_t* work, uint32_t* err,
                     void* stream) {
   const char* why = kvp_check(p);
   if (!*why) why = kvp_check_cache(p, c);
   if (!*why && !work) why = "work is NULL";
+  if (!*why && ((uintptr_t)n_live & 7)) why = "n_live must be 8-byte aligned";
   if (*why) return kvp_refuse("gpt_kv8_compact", why);
   const Kv8PoolP P = kvp_pool(*p, err);
   const Kv8CopyP C = kvp_copy(*c);
