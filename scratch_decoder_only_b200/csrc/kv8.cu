@@ -254,42 +254,54 @@ __global__ void __launch_bounds__(128) kv8_read_kernel(Kv8ReadP p) {
 }
 
 // ---------------------------------------------------------------------------
-// Attention.  In x_t = scale * q . k_t (per key/value head, its G query heads
-// and the sequence's n newest tokens are nG queries of one key row) a tile is
-// 64 tokens by NQ = 8 NT queries.  One pass over the tokens with a running
-// maximum m and sum l per query (base-2 exponents).
+// Attention.  Per key/value head, its G query heads and the sequence's n newest
+// tokens are nG queries of one row of keys; a job is NQ = 8 NT of them, and its
+// work is tiles of TILE tokens, in one pass with a running maximum m and sum l
+// per query (base-2 exponents).
 //
 // Bound: one byte per key and value channel from HBM, about 23 bytes a cycle
 // and SM, each of which has to be widened.  So the product with the fewest
 // instructions per byte is taken: mma m16n8k16 on f16 with the TOKENS as its
 // 16 rows (scores^T = K Q^T, out^T = V^T W^T), so that eight queries fill the
-// instruction and a single query wastes no exponentials on empty token rows.
-// Codes go from global memory to the operand registers without shared memory:
-// which k index of the instruction stands for which channel (or token) is free
-// as long as both operands agree, so lane (c, t) = (lane / 4, lane % 4) takes
-// quarter t of a key's channels, and for values the 16 tokens of 16-token
-// group t of the tile, one 16-byte load each (the layout of v is made for
-// it).  Score row c of an instruction is then a token of group c / 2, all of
-// one page: its two scales are one register each.  The weights reach the
-// layout of the second product's B operand by an 8x8 transpose (movmatrix).
+// instruction and a single query wastes no exponentials on empty rows.  Which
+// k index of the instruction stands for which channel (or token) is free as
+// long as both operands agree, so lane (c, t) = (lane / 4, lane % 4) takes
+// quarter t of a key's channels, and for values the t-th quarter of the tile's
+// tokens, 16 bytes a load either way (the layout of v is made for it).  Score
+// row c of an instruction is then a token of quarter c / 2, all in one page:
+// its two scales are one register each.  The weights reach the layout of the
+// second product's B operand by an 8x8 transpose (movmatrix).  The maximum is
+// brought up to date only when a score passes it by 2^8 (w <= 256 in f16), so
+// most tiles need no reduction over lanes and no rescaling.
+//
+// Latency: the codes of a warp's next tile travel by asynchronous copies into
+// shared memory while it works on the present one; the page ids of the tile
+// after that are being loaded.  Lanes copy whole 128-byte lines (an
+// asynchronous copy whose eight lanes lie in different lines is taken apart lane by
+// lane) to places permuted so that the reads above have no bank conflicts.
+// Three blocks of four warps an SM keep about 100 KB in flight; warps meet no
+// barrier while they run.
 //
 // Rounding: q is taken to f16 with a power of two of its own per query, which
-// keeps all of bf16's and f16's bits down to 2^-28 of the query's largest
-// element (2^-24 of the largest for fp16, where the power is 1); codes are
-// exact in f16; scores, m, l and the output sum are fp32.  Only the weights
-// lose bits: w * (page's value scale) / (largest value scale so far) is at
-// most 1 and rounded to f16 (2^-12 relative, below the output's own 2^-9 or
-// 2^-12), and the output accumulates in units of that largest scale.
+// keeps all of bf16's bits down to 2^-28 of the query's largest element (fp16
+// queries are f16); codes are exact in f16; scores, m, l and the output sum are
+// fp32.  Only the weights lose bits: w * (page's value scale) / (largest value
+// scale so far) is rounded to f16 (2^-12 relative, below the output's own 2^-9
+// or 2^-12), and the output sum is in units of that scale.
 //
-// Split: (64-query job, head) pairs may be few and a context long, so its
-// tiles are cut into up to S pieces, one block of four warps each (the warps
-// take tiles in turn, and merge their m, l and sums in shared memory in a fixed
-// order); with more than one piece, fp32 partials go to scratch and a second
-// kernel merges them, again in a fixed order.  S comes from the host's bound on
-// the lengths, the pieces in use from the device's lengths: at least MINT tiles each.
+// Split: lengths are known on the device only, and a batch may mix a few tokens
+// with a hundred thousand.  So the tiles of all (sequence, NQ queries, head)
+// jobs are numbered, KV8_OVER units ahead of each job's first for what a job
+// costs besides its tiles, and each warp of the grid's resident blocks takes an
+// equal run of units.  A job that a run cuts leaves fp32 partials in scratch,
+// two at most per run, and a second kernel merges them in a fixed order, its
+// columns spread over the warps whose runs have a piece.  Where the host knows
+// that jobs are short (KV8_WHOLE tiles at most), a block takes a whole job, its
+// four warps the tiles in turn, and merges it in shared memory: one kernel.
 // ---------------------------------------------------------------------------
 #define KV8_NW 4
-#define KV8_MINT 4
+#define KV8_WHOLE 8
+#define KV8_OVER 2
 
 struct Kv8AttnP {
   Kv8Layer L;
@@ -298,9 +310,9 @@ struct Kv8AttnP {
   uint16_t* out;
   float* lse;
   long ldq, ldo;
-  int H, G, S;
+  int H, G, cap;
   float scale;
-  float *part, *part_ml;   // [job][Hkv][S][NQ][D] sums, [..][NQ][2] (m, l)
+  float *part, *part_ml;   // [run][2][NQ][D] sums, [run][2][NQ][2] (m, l)
   unsigned* err;
 };
 
@@ -321,377 +333,672 @@ __device__ __forceinline__ uint32_t kv8_transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-
-// A job: NQ queries of one sequence and key/value head, numbered (row of the
-// sequence) * G + (query head of the group).
-struct Kv8Job {
-  int b, s0, n, len, q0, nq;   // first query, valid queries (nq < 1: no such job)
-  int maxlim;                  // tokens that its last query sees, within the row's pages
-  int chunk, pieces;           // tiles a piece, pieces in use
-};
-template <int NQ>
-__device__ __forceinline__ bool kv8_job(const Kv8AttnP& p, int job, Kv8Job& J, unsigned* err) {
-  Kv8Seq s;
-  int off;
-  if (p.q.start) {
-    const int G = p.G;
-    if (!kv8_find(p.q, job, [G](int b, int s0) { return (int)((long)s0 * G / NQ) + b; }, s, off, err)) return false;
-  } else {
-    const int per = (p.G + NQ - 1) / NQ;
-    s.b = s.s0 = job / per; s.n = 1; s.len = p.q.lens[s.b];
-    off = job % per;
-  }
-  J.b = s.b; J.s0 = s.s0; J.n = s.n; J.len = s.len;
-  J.q0 = off * NQ;
-  J.nq = min(NQ, s.n * p.G - J.q0);
-  if (J.nq < 1) return false;
-  const int cap = p.q.max_pages << p.L.lp;
-  if (off == 0 && threadIdx.x == 0 && (s.len < s.n || s.len > cap)) set_dev_err(err, GPT_DEVERR_POS);
-  const int last = (J.q0 + J.nq - 1) / p.G;
-  J.maxlim = min(max(s.len - s.n + last + 1, 0), cap);
-  const int tiles = (J.maxlim + 63) >> 6;
-  const int want = max(1, min(p.S, (tiles + KV8_MINT - 1) / KV8_MINT));
-  J.chunk = max(1, (tiles + want - 1) / want);
-  J.pieces = max(1, (tiles + J.chunk - 1) / J.chunk);
-  return true;
+// N bytes, or N zeros
+template <int N>
+__device__ __forceinline__ void kv8_copy(uint32_t dst, const uint8_t* src, bool on) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(on ? N : 0), "n"(N)
+                 : "memory");
 }
-
-// keep the low n bytes (0..16) of 16
+template <int N>
+__device__ __forceinline__ void kv8_lds(uint32_t* r, uint32_t src) {
+  if constexpr (N == 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(src) : "memory");
+  else if constexpr (N == 8) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(src) : "memory");
+  else
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(src) : "memory");
+}
+// keep the low n bytes of four
 __device__ __forceinline__ uint32_t kv8_low_bytes(uint32_t w, int n) {
   return n >= 4 ? w : n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u);
 }
 
-template <typename T, int D, int NT, int KIND>
+// A sequence's share of the work: jobs = ceil(n G / NQ) * heads, tiles a job
+// (an empty sequence has one, for its rows' zeros).
+struct Kv8Share {
+  int s0, n, len, jobs, tiles;
+};
+template <int NQ, int TILE>
+__device__ __forceinline__ Kv8Share kv8_share(const Kv8AttnP& p, int b) {
+  Kv8Share s;
+  if (p.q.start) {
+    s.s0 = min(max(p.q.start[b], 0), p.q.rows);
+    s.n = min(max(p.q.start[b + 1], s.s0), p.q.rows) - s.s0;
+  } else {
+    s.s0 = b;
+    s.n = 1;
+  }
+  s.len = p.q.lens[b];
+  s.jobs = (int)(((long)s.n * p.G + NQ - 1) / NQ) * p.L.Hkv;
+  s.tiles = max(1, (min(max(s.len, 0), p.cap) + TILE - 1) / TILE);
+  return s;
+}
+
+// Where this warp's run begins (WHOLE: where the block's job is): the sequence,
+// its job, the unit in the job.  Run number blockIdx.x * KV8_NW + warp covers
+// units [run * quota, (run + 1) * quota) of total.  All threads of the block call
+// this; false: no such run.
+struct Kv8Run {
+  int b, job, x;
+  long u, quota, total;
+};
+template <int NQ, int TILE, bool WHOLE>
+__device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, Kv8Run& r) {
+  __shared__ long wsum[KV8_NW], sh_rem[KV8_NW];
+  __shared__ int sh_b[KV8_NW];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.q.B;
+  auto units = [&](int b) -> long {
+    if (b >= B) return 0;
+    const Kv8Share s = kv8_share<NQ, TILE>(p, b);
+    return WHOLE ? s.jobs : (long)s.jobs * (s.tiles + KV8_OVER);
+  };
+  const long mine = units(tid);   // of the first 128 sequences
+  r.total = 0;
+  r.quota = 1;
+  long u0 = blockIdx.x;
+  if (!WHOLE) {
+    long sum = mine;
+    for (int b = tid + 32 * KV8_NW; b < B; b += 32 * KV8_NW) sum += units(b);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    if (lane == 0) wsum[warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < KV8_NW; ++w) r.total += wsum[w];
+    const long runs = (long)gridDim.x * KV8_NW;
+    r.quota = max((long)KV8_OVER + 1, (r.total + runs - 1) / runs);
+    u0 = (long)blockIdx.x * KV8_NW * r.quota;
+    if (u0 >= r.total) return false;
+    if (tid < KV8_NW) sh_b[tid] = -1;
+  }
+  r.u = WHOLE ? u0 : u0 + warp * r.quota;
+  const long u3 = WHOLE ? u0 : min(u0 + (KV8_NW - 1) * r.quota, r.total - 1);
+  long carry = 0;
+  for (int b0 = 0; b0 < B; b0 += 32 * KV8_NW) {
+    const long v = b0 ? units(b0 + tid) : mine;
+    long inc = v;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const long y = __shfl_up_sync(0xffffffffu, inc, k);
+      if (lane >= k) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    long first = carry + inc - v;
+    for (int w = 0; w < KV8_NW; ++w) {
+      if (w < warp) first += wsum[w];
+      carry += wsum[w];
+    }
+    for (int w = 0; w < (WHOLE ? 1 : KV8_NW); ++w) {
+      const long u = u0 + w * r.quota;
+      if (u >= first && u < first + v) {
+        sh_b[w] = b0 + tid;
+        sh_rem[w] = u - first;
+      }
+    }
+    if (carry > u3) break;
+  }
+  if (WHOLE && carry <= u0) return false;
+  __syncthreads();
+  r.b = sh_b[WHOLE ? 0 : warp];
+  const long rem = sh_rem[WHOLE ? 0 : warp];
+  if (WHOLE) {
+    r.job = (int)rem;
+    r.x = KV8_OVER;
+  } else if (r.b >= 0) {
+    const int w = kv8_share<NQ, TILE>(p, r.b).tiles + KV8_OVER;
+    r.job = (int)(rem / w);
+    r.x = (int)(rem % w);
+  }
+  return true;
+}
+
+template <int D>
+struct Kv8Tile {
+  static constexpr int TILE = D == 128 ? 32 : 64;
+  static constexpr int STAGE = TILE * D * 2;   // bytes a warp copies at a time
+};
+template <int D, int NT, bool WHOLE>
+constexpr size_t kv8_attn_smem() {
+  return (size_t)KV8_NW * 2 * Kv8Tile<D>::STAGE + (WHOLE ? (size_t)2 * 8 * NT * (D + 4) * 4 : 0);
+}
+
+// The result of query q0 + n of a job, four channels from d on.
+template <typename T>
+__device__ __forceinline__ void kv8_out(const Kv8AttnP& p, int s0, int h, int qi, int d, int D, float4 y, float M,
+                                        float lt) {
+  const int row = s0 + qi / p.G, hq = h * p.G + qi % p.G;
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  union { T v[4]; uint2 u; } z;
+  z.v[0] = from_f<T>(y.x * inv); z.v[1] = from_f<T>(y.y * inv);
+  z.v[2] = from_f<T>(y.z * inv); z.v[3] = from_f<T>(y.w * inv);
+  *reinterpret_cast<uint2*>(p.out + (long)row * p.ldo + hq * D + d) = z.u;
+  if (d == 0 && p.lse) p.lse[(long)row * p.H + hq] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * 0.6931471805599453f;
+}
+
+template <typename T, int D, int NT, int KIND, bool WHOLE>
 __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
-  constexpr int NQ = 8 * NT, KW = D / 16, ROW = D + 4;
+  constexpr int NQ = 8 * NT, KW = D / 16, ROW = D + 4, TILE = Kv8Tile<D>::TILE, STAGE = Kv8Tile<D>::STAGE;
+  constexpr int TQ = TILE / 4;                         // tokens of a quarter
+  constexpr int KP = D / 4 < 16 ? D / 4 : 16, KT = D / 4 / KP;   // bytes of a key read, reads of a quarter key
+  constexpr int STEP = WHOLE ? KV8_NW : 1;
   griddep_wait();
   griddep_release();
-  __shared__ __align__(16) float so[KV8_NW][NQ][ROW];
-  __shared__ float sm[KV8_NW][NQ], sl[KV8_NW][NQ];
+  extern __shared__ __align__(128) uint8_t ring[];
   const Kv8Layer& L = p.L;
-  const int job = blockIdx.x / p.S, piece = blockIdx.x % p.S, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane >> 2, t = lane & 3;
-  Kv8Job J;
-  if (!kv8_job<NQ>(p, job, J, h == 0 && piece == 0 ? p.err : nullptr) || piece >= J.pieces) return;
-  const int G = p.G, lp = L.lp;
+  const int G = p.G, lp = L.lp, pmask = (1 << lp) - 1, Hkv = L.Hkv;
   const long pd = (long)D << lp;
-
-  // ---- queries: operand registers, score factors of this lane's two columns, tokens they see
-  uint32_t qf[NT][KW][2];
-  float cq[NT][2];
-  int lim[NT][2], minlim = 0x7fffffff;
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int qi = J.q0 + j * 8 + c;
-    const bool ok = j * 8 + c < J.nq;
-    float f[D / 4], mx = 0.f;
-    if (ok) {
-      const int i = qi / G;
-      const uint16_t* x = p.x + (long)(J.s0 + i) * p.ldq + (h * G + qi - i * G) * D + t * (D / 4);
-#pragma unroll
-      for (int e = 0; e < D / 4; e += 4) {
-        const uint2 w = *reinterpret_cast<const uint2*>(x + e);
-        f[e] = bits16_f<T>(w.x & 0xffffu); f[e + 1] = bits16_f<T>(w.x >> 16);
-        f[e + 2] = bits16_f<T>(w.y & 0xffffu); f[e + 3] = bits16_f<T>(w.y >> 16);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < D / 4; ++e) f[e] = 0.f;
-    }
-    bool bad = false;
-#pragma unroll
-    for (int e = 0; e < D / 4; ++e) {
-      bad |= !(fabsf(f[e]) <= FLT_MAX);
-      mx = fmaxf(mx, fabsf(f[e]));
-    }
-    float up = 1.f;
-    if constexpr (sizeof(T) == 2 && !std::is_same<T, f16>::value) {
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // the power of two that brings the largest element to [16, 32)
-      const int ex = (__float_as_int(mx) >> 23) & 255;
-      up = __int_as_float(max(1, min(254, 258 - max(ex, 1))) << 23);
-    }
-    bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 28) & 15u) != 0;   // of the query's four lanes
-    const float fac = bad ? NAN : p.scale * 1.4426950408889634f * (1.f / up);
-#pragma unroll
-    for (int w = 0; w < KW; ++w) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const __half2 v = __floats2half2_rn(bad ? 0.f : f[4 * w + 2 * e] * up, bad ? 0.f : f[4 * w + 2 * e + 1] * up);
-        qf[j][w][e] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-    }
-    // columns 2t, 2t + 1 of the accumulators are the queries held by lanes 8t and 8t + 4
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      cq[j][e] = __shfl_sync(0xffffffffu, fac, 8 * t + 4 * e);
-      const int n = j * 8 + 2 * t + e;
-      lim[j][e] = n < J.nq ? min(max(J.len - J.n + (J.q0 + n) / G + 1, 0), J.maxlim) : J.maxlim;
-      minlim = min(minlim, lim[j][e]);
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < p.q.B; b += 32 * KV8_NW) {
+      if (p.q.start && (p.q.start[b] < 0 || p.q.start[b + 1] < p.q.start[b] || p.q.start[b + 1] > p.q.rows))
+        set_dev_err(p.err, GPT_DEVERR_START);
+      const Kv8Share s = kv8_share<NQ, TILE>(p, b);
+      if (s.n && (s.len < s.n || s.len > p.cap)) set_dev_err(p.err, GPT_DEVERR_POS);
     }
   }
-  minlim = min(minlim, __shfl_xor_sync(0xffffffffu, minlim, 1));
-  minlim = min(minlim, __shfl_xor_sync(0xffffffffu, minlim, 2));
+  Kv8Run r;
+  if (!kv8_locate<NQ, TILE, WHOLE>(p, r)) return;
+  if (!WHOLE && (r.u >= r.total || r.b < 0)) return;   // no barrier follows
+  Kv8Share sh = kv8_share<NQ, TILE>(p, r.b);
+  // units of this run, counted from its begin; a job's first KV8_OVER have no tile
+  const int R = WHOLE ? sh.tiles : (int)min(r.quota, r.total - r.u);
 
-  float o[NT][KW][4], m[NT][2], l[NT][2], vref = 0.f;
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-#pragma unroll
-    for (int i = 0; i < KW; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][i][e] = 0.f;
-    m[j][0] = m[j][1] = -INFINITY;
-    l[j][0] = l[j][1] = 0.f;
+  // ---- the warp's next tile: sequence nb, head nh, tile nt of nm, the job's number nj of njobs; the page of
+  // this lane's quarter (-1: none); nu: the unit
+  int nb = r.b, nj = r.job, nh = r.job % Hkv, nt = r.x - KV8_OVER, nm = sh.tiles, njobs = sh.jobs;
+  int nlen = min(max(sh.len, 0), p.cap), nid = -1, nu = 0;
+  if (nt < 0) {
+    nu = -nt;
+    nt = 0;
   }
-
-  const int t1 = min((J.maxlim + 63) >> 6, (piece + 1) * J.chunk);
-  const int* row = p.q.table + (long)J.b * p.q.ld_table;
-  for (int tile = piece * J.chunk + warp; tile < t1; tile += KV8_NW) {
-    const int tb = tile << 6, gv = tb + 16 * t, gk = tb + 16 * (c >> 1);
-    // pages of the tile's four 16-token groups: group t in lane t
-    int id = -1;
-    if (gv < J.maxlim) {
-      id = row[gv >> lp];
-      if ((unsigned)id >= (unsigned)L.n_pages) {
+  auto page = [&]() {
+    const int tok = nt * TILE + TQ * t;
+    nid = -1;
+    if (nu < R && tok < nlen) {
+      nid = p.q.table[(long)nb * p.q.ld_table + (tok >> lp)];
+      if ((unsigned)nid >= (unsigned)L.n_pages) {
         set_dev_err(p.err, GPT_DEVERR_PAGE);
-        id = -1;
+        nid = -1;
       }
     }
-    const int idk = __shfl_sync(0xffffffffu, id, c >> 1);
-    // ---- loads: 8 keys' quarters, 2 KW channels' 16 tokens
-    uint32_t kr[8][KW], vr[2 * KW][4];
-    float ks = 0.f, vs = 0.f;
-    if (idk >= 0) {
-      const size_t ph = (size_t)idk * L.Hkv + h;
-      const uint8_t* kp = L.k + ph * pd + ((gk & ((1 << lp) - 1)) + (c & 1)) * D + t * (D / 4);
+  };
+  auto advance = [&]() {
+    nu += STEP;
+    nt += STEP;
+    if (!WHOLE && nt >= nm) {
+      nu += KV8_OVER;
+      nt = 0;
+      if (++nh == Hkv) nh = 0;
+      if (++nj == njobs && nu < R) {
+        Kv8Share s;
+        do {
+          if (++nb >= p.q.B) {   // only where lens changed meanwhile
+            nu = R;
+            break;
+          }
+          s = kv8_share<NQ, TILE>(p, nb);
+        } while (s.jobs == 0);
+        if (nu < R) {
+          nj = 0;
+          nm = s.tiles;
+          njobs = s.jobs;
+          nlen = min(max(s.len, 0), p.cap);
+        }
+      }
+    }
+    page();
+  };
+  const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + warp * 2 * STAGE;
+  float ks_next = 0.f, vs_next = 0.f;
+  int id_next = -1;
+  // Keys lie in a stage token by token, values by group of 16 tokens and
+  // channel, 16 bytes a piece.  Bits 4 to 6 of the address are exchanged by
+  // exclusive or within a 128-byte line so that the eight lanes of a 16-byte read (16 of an
+  // 8-byte, 32 of a 4-byte one) meet eight (16, 32) different bank groups.
+  auto fetch = [&](int stage) {
+    if (nu < R) {
+      const int tb = nt * TILE;
+      const uint32_t s0 = ring0 + stage * STAGE;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint8_t* a = kp + 2 * i * D;
-        if constexpr (KW == 1) kr[i][0] = *reinterpret_cast<const uint32_t*>(a);
-        else if constexpr (KW == 2) {
-          const uint2 w = *reinterpret_cast<const uint2*>(a);
-          kr[i][0] = w.x; kr[i][1] = w.y;
-        } else {
+      for (int g = 0; g < TILE / 16; ++g) {
+        // group g of the tile: 16 tokens of one page
+        const int id = __shfl_sync(0xffffffffu, nid, g * (16 / TQ));
+        const size_t ph = (size_t)max(id, 0) * Hkv + nh;
+        const long at = ph * pd + ((tb + 16 * g) & pmask) * D + lane * 16;
+        const bool on = id >= 0;
+        constexpr int N = D / 32 ? D / 32 : 1;   // copies of 32 lanes a group
+        const bool mine = D >= 32 || lane < 16;
+        const uint32_t kx = D == 128 ? (lane >> 3 & 1) << 6 : D == 64 ? 0 : (g & (64 / D - 1)) * 2 * D;
+        const uint32_t vx = TQ == 16 ? (g & 3) << 5 : (g & 1) << 6;
 #pragma unroll
-          for (int w4 = 0; w4 < KW; w4 += 4) {
-            const uint4 w = *reinterpret_cast<const uint4*>(a + 4 * w4);
-            kr[i][w4] = w.x; kr[i][w4 + 1] = w.y; kr[i][w4 + 2] = w.z; kr[i][w4 + 3] = w.w;
+        for (int i = 0; i < N; ++i) {
+          if (mine) {
+            kv8_copy<16>(s0 + g * 16 * D + i * 512 + (lane * 16 ^ kx), L.k + at + i * 512, on);
+            kv8_copy<16>(s0 + TILE * D + g * 16 * D + i * 512 + (lane * 16 ^ vx), L.v + at + i * 512, on);
           }
         }
       }
-      ks = L.ks[ph];
-      vs = L.vs[ph];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int w = 0; w < KW; ++w) kr[i][w] = 0;
+      const int idk = __shfl_sync(0xffffffffu, nid, c >> 1);
+      const size_t phk = (size_t)max(idk, 0) * Hkv + nh;
+      ks_next = idk >= 0 ? L.ks[phk] : 0.f;
+      vs_next = idk >= 0 ? L.vs[phk] : 0.f;
     }
-    if (id >= 0) {
-      const uint8_t* vp = L.v + ((size_t)id * L.Hkv + h) * pd + (gv & ((1 << lp) - 1)) * D + c * 16;
+    id_next = nid;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (WHOLE) {
+    nu += warp;
+    nt += warp;
+  }
+  page();
+  fetch(0);
+  advance();
+
+  // ---- this lane's read offsets in a stage
+  // keys: token TQ (c / 2) + (c & 1) + 2 i, bytes t D / 4 .. (128 channels: 16 t .. and 64 + 16 t ..); the bits of
+  // 2 i D are 0 in koff's place of them before the exchange, so they join by exclusive or where both meet (D < 64)
+  uint32_t koff, voff;
+  {
+    const int tk = TQ * (c >> 1) + (c & 1);
+    if constexpr (D == 128) koff = tk * D + (t * 16 ^ (tk & 1) << 6);
+    else koff = tk * D + t * (D / 4);
+    if constexpr (D < 64) koff ^= (tk >> 4 & (64 / D - 1)) * 2 * D;
+    const int g = t * TQ >> 4;
+    voff = TILE * D + g * 16 * D + (c * 16 ^ (TQ == 16 ? g << 5 : g << 6)) + (t * TQ & 15);
+  }
+  int stage = 0, cu = WHOLE ? warp : max(0, KV8_OVER - r.x);
+  int b = r.b, job = r.job, x = r.x;
+  for (int su = 0; su < R;) {
+    // ---- one job of the run: units [su, su + span), tiles [tile0, tile0 + cnt)
+    const int tile0 = max(0, x - KV8_OVER), skip = max(0, KV8_OVER - x);
+    const int span = WHOLE ? R : min(sh.tiles + KV8_OVER - x, R - su), cnt = span - skip;
+    if (!WHOLE && cnt <= 0) break;   // the run ends ahead of the job's tiles
+    const int h = job % Hkv, q0 = job / Hkv * NQ, nq = min(NQ, sh.n * G - q0), slen = min(max(sh.len, 0), p.cap);
+    // queries: operand registers, score factors of this lane's two columns, tokens they see
+    uint32_t qf[NT][KW][2];
+    float cq[NT][2];
+    int lim[NT][2], minlim = 0x7fffffff;
 #pragma unroll
-      for (int i = 0; i < 2 * KW; ++i) {
-        const uint4 w = *reinterpret_cast<const uint4*>(vp + i * 128);
-        vr[i][0] = w.x; vr[i][1] = w.y; vr[i][2] = w.z; vr[i][3] = w.w;
+    for (int j = 0; j < NT; ++j) {
+      const int qi = q0 + j * 8 + c;
+      const bool ok = j * 8 + c < nq;
+      float f[D / 4], mx = 0.f;
+      if (ok) {
+        const int i = qi / G;
+        const uint16_t* y = p.x + (long)(sh.s0 + i) * p.ldq + (h * G + qi - i * G) * D + t * (D == 128 ? 16 : D / 4);
+#pragma unroll
+        for (int e = 0; e < D / 4; e += 4) {
+          const uint2 w = *reinterpret_cast<const uint2*>(y + e + (D == 128 && e >= 16 ? 48 : 0));
+          f[e] = bits16_f<T>(w.x & 0xffffu); f[e + 1] = bits16_f<T>(w.x >> 16);
+          f[e + 2] = bits16_f<T>(w.y & 0xffffu); f[e + 3] = bits16_f<T>(w.y >> 16);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < D / 4; ++e) f[e] = 0.f;
       }
-    } else {
+      bool bad = false;
 #pragma unroll
-      for (int i = 0; i < 2 * KW; ++i) vr[i][0] = vr[i][1] = vr[i][2] = vr[i][3] = 0;
-    }
-    const bool whole = tb + 64 <= minlim && !__any_sync(0xffffffffu, id < 0);
-    if (!whole) {
-      // unwritten slots may hold any byte, also e4m3's NaN: 0 * NaN must not reach the sums
-#pragma unroll
-      for (int i = 0; i < 2 * KW; ++i)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) vr[i][w] = kv8_low_bytes(vr[i][w], J.maxlim - gv - 4 * w);
-    }
-    // ---- scores^T: s[i][j][e + 2 r] is token gk + (c & 1) + 4 i + 2 r with query 8 j + 2 t + e
-    float s[4][NT][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.f;
+      for (int e = 0; e < D / 4; ++e) {
+        bad |= !(fabsf(f[e]) <= FLT_MAX);
+        mx = fmaxf(mx, fabsf(f[e]));
+      }
+      float up = 1.f;
+      if constexpr (!std::is_same<T, f16>::value) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // the power of two that brings the largest element to [16, 32)
+        const int ex = (__float_as_int(mx) >> 23) & 255;
+        up = __int_as_float(max(1, min(254, 258 - max(ex, 1))) << 23);
+      }
+      bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 28) & 15u) != 0;   // of the query's four lanes
+      const float fac = bad ? NAN : p.scale * 1.4426950408889634f * (1.f / up);
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        uint32_t a[4];
-        kv8_widen<KIND>(kr[2 * i][w], a[0], a[2]);
-        kv8_widen<KIND>(kr[2 * i + 1][w], a[1], a[3]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) kv8_mma(s[i][j], a, qf[j][w]);
+        for (int e = 0; e < 2; ++e) {
+          const __half2 v = __floats2half2_rn(bad ? 0.f : f[4 * w + 2 * e] * up, bad ? 0.f : f[4 * w + 2 * e + 1] * up);
+          qf[j][w][e] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+      }
+      // columns 2t, 2t + 1 of the accumulators are the queries held by lanes 8t and 8t + 4
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        cq[j][e] = __shfl_sync(0xffffffffu, fac, 8 * t + 4 * e);
+        const int n = j * 8 + 2 * t + e;
+        lim[j][e] = n < nq ? min(max(sh.len - sh.n + (q0 + n) / G + 1, 0), slen) : slen;
+        minlim = min(minlim, lim[j][e]);
       }
     }
-    float tv = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 8));
-    tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 16));
-    const float vnew = fmaxf(vref, tv), vinv = vnew > 0.f ? 1.f / vnew : 0.f;
-    const float vfac = vnew > 0.f ? vs * vinv : vs, vold = vnew > 0.f ? vref * vinv : 1.f;
-    vref = vnew;
-    uint32_t wf[4][NT][2];
+    minlim = min(minlim, __shfl_xor_sync(0xffffffffu, minlim, 1));
+    minlim = min(minlim, __shfl_xor_sync(0xffffffffu, minlim, 2));
+
+    float o[NT][KW][4], m[NT][2], l[NT][2], vref = 0.f, vinv = 0.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float fac = cq[j][e] * ks;
-        float x[8], mx = -INFINITY;
+      for (int i = 0; i < KW; ++i)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = s[i >> 1][j][e + 2 * (i & 1)] * fac;
-          if (!whole && (gk + (c & 1) + 2 * i >= lim[j][e] || idk < 0)) x[i] = -INFINITY;
-          mx = fmaxf(mx, x[i]);
-        }
+        for (int e = 0; e < 4; ++e) o[j][i][e] = 0.f;
+      m[j][0] = m[j][1] = -INFINITY;
+      l[j][0] = l[j][1] = 0.f;
+    }
+
+    for (; cu < su + span; cu += STEP) {
+      const int id = id_next;
+      const float ks = ks_next, vs = vs_next;
+      __syncwarp();   // the stage of the tile before has been read by all lanes
+      fetch(stage ^ 1);
+      advance();
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      const uint32_t s0 = ring0 + stage * STAGE;
+      stage ^= 1;
+      const int tb = (tile0 + cu - su - skip) * TILE, gv = tb + TQ * t, gk = tb + TQ * (c >> 1);
+      const bool full = !__any_sync(0xffffffffu, id < 0) && tb + TILE <= minlim;
+      // ---- scores^T: s[i][j][e + 2 r] is token gk + (c & 1) + 4 i + 2 r with query 8 j + 2 t + e
+      float s[TQ / 4][NT][4];
 #pragma unroll
-        for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-        const float mn = fmaxf(m[j][e], mx), mu = mn == -INFINITY ? 0.f : mn;
-        const float al = kv8_ex2(m[j][e] - mu);
-        m[j][e] = mn;
-        float sum = 0.f;
+      for (int i = 0; i < TQ / 4; ++i) {
+        uint32_t kr[2][KW];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float w = kv8_ex2(x[i] - mu);
-          sum += w;
-          s[i >> 1][j][e + 2 * (i & 1)] = x[i] == -INFINITY ? 0.f : w * vfac;
-        }
-        l[j][e] = l[j][e] * al + sum;
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          o[j][i][e] *= al * vold;
-          o[j][i][e + 2] *= al * vold;
+          for (int w = 0; w < KT; ++w) {
+            const uint32_t at = w ? koff ^ 64 : koff, more = (4 * i + 2 * e) * D;
+            kv8_lds<KP>(&kr[e][w * 4], s0 + (D < 64 ? at ^ more : at + more));
+          }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint32_t a[4];
+          kv8_widen<KIND>(kr[0][w], a[0], a[2]);
+          kv8_widen<KIND>(kr[1][w], a[1], a[3]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) kv8_mma(s[i][j], a, qf[j][w]);
         }
       }
+      float fac[NT][2];
+      bool stale = !full || vs > vref;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const __half2 w = __floats2half2_rn(s[i][j][2 * e], s[i][j][2 * e + 1]);
-          wf[i][j][e] = kv8_transpose8(*reinterpret_cast<const uint32_t*>(&w));
+          fac[j][e] = cq[j][e] * ks;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < TQ / 2; ++i) mx = fmaxf(mx, fmaf(s[i >> 1][j][e + 2 * (i & 1)], fac[j][e], -m[j][e]));
+          stale |= mx > 8.f;
         }
-    }
-    // ---- out^T += V^T W^T
+      const bool kon = __shfl_sync(0xffffffffu, id, c >> 1) >= 0;
+      if (__any_sync(0xffffffffu, stale)) {
+        float tv = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 8));
+        tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 16));
+        const float vnew = fmaxf(vref, tv);
+        vinv = vnew > 0.f ? 1.f / vnew : 1.f;   // (all scales 0, or NaN: they stay what they are)
+        const float vold = vnew > 0.f ? vref * vinv : 1.f;
+        vref = vnew;
 #pragma unroll
-    for (int k = 0; k < KW; ++k)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t a[4];
-        kv8_widen<KIND>(vr[2 * k][i], a[0], a[2]);
-        kv8_widen<KIND>(vr[2 * k + 1][i], a[1], a[3]);
+          for (int e = 0; e < 2; ++e) {
+            float mx = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) kv8_mma(o[j][k], a, wf[i][j]);
+            for (int i = 0; i < TQ / 2; ++i) {
+              const float y = s[i >> 1][j][e + 2 * (i & 1)] * fac[j][e];
+              if (full || (gk + (c & 1) + 2 * i < lim[j][e] && kon)) mx = fmaxf(mx, y);
+            }
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+            const float mn = fmaxf(m[j][e], mx), al = kv8_ex2(m[j][e] - (mn == -INFINITY ? 0.f : mn));
+            m[j][e] = mn;
+            l[j][e] *= al;
+#pragma unroll
+            for (int i = 0; i < KW; ++i) {
+              o[j][i][e] *= al * vold;
+              o[j][i][e + 2] *= al * vold;
+            }
+          }
       }
-  }
+      const float vfac = vs * vinv;
+      uint32_t wf[TQ / 4][NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mu = m[j][e] == -INFINITY ? 0.f : m[j][e];
+#pragma unroll
+          for (int i = 0; i < TQ / 2; ++i) {
+            float& y = s[i >> 1][j][e + 2 * (i & 1)];
+            const float w = kv8_ex2(fmaf(y, fac[j][e], -mu));
+            // a token that is not seen weighs 0 even where its page's scale is NaN
+            if (full || (gk + (c & 1) + 2 * i < lim[j][e] && kon)) {
+              l[j][e] += w;
+              y = w * vfac;
+            } else {
+              y = 0.f;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < TQ / 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const __half2 w = __floats2half2_rn(s[i][j][2 * e], s[i][j][2 * e + 1]);
+            wf[i][j][e] = kv8_transpose8(*reinterpret_cast<const uint32_t*>(&w));
+          }
+      }
+      // ---- out^T += V^T W^T
+#pragma unroll
+      for (int k = 0; k < KW; ++k) {
+        uint32_t vr[2][TQ / 4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          kv8_lds<TQ>(vr[e], s0 + voff + (2 * k + e) * 128);
+          if (!full) {
+            // unwritten slots may hold any byte, also e4m3's NaN: 0 * NaN must not reach the sums
+#pragma unroll
+            for (int w = 0; w < TQ / 4; ++w) vr[e][w] = kv8_low_bytes(vr[e][w], slen - gv - 4 * w);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < TQ / 4; ++i) {
+          uint32_t a[4];
+          kv8_widen<KIND>(vr[0][i], a[0], a[2]);
+          kv8_widen<KIND>(vr[1][i], a[1], a[3]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) kv8_mma(o[j][k], a, wf[i][j]);
+        }
+      }
+    }
 
-  // ---- merge the warps
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int n = j * 8 + 2 * t + e;
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int k = 4; k < 32; k <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], k);
+        for (int k = 4; k < 32; k <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], k);
 #pragma unroll
-      for (int i = 0; i < KW; ++i) {
-        so[warp][n][i * 16 + c] = o[j][i][e] * vref;
-        so[warp][n][i * 16 + c + 8] = o[j][i][e + 2] * vref;
+        for (int i = 0; i < KW; ++i) {
+          o[j][i][e] *= vref;
+          o[j][i][e + 2] *= vref;
+        }
       }
-      if (c == 0) {
-        sm[warp][n] = m[j][e];
-        sl[warp][n] = l[j][e];
+    if constexpr (WHOLE) {
+      // ---- merge the warps: 2, 3 into 0, 1, then 1 into 0, whose result goes out
+      float* so = reinterpret_cast<float*>(ring + KV8_NW * 2 * STAGE);   // [2][NQ][ROW]
+      __shared__ float sm[2][NQ], sl[2][NQ];
+      auto put = [&](int at) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int n = j * 8 + 2 * t + e;
+#pragma unroll
+            for (int i = 0; i < KW; ++i) {
+              so[(at * NQ + n) * ROW + i * 16 + c] = o[j][i][e];
+              so[(at * NQ + n) * ROW + i * 16 + c + 8] = o[j][i][e + 2];
+            }
+            if (c == 0) {
+              sm[at][n] = m[j][e];
+              sl[at][n] = l[j][e];
+            }
+          }
+      };
+      auto take = [&](int at) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int n = j * 8 + 2 * t + e;
+            const float m2 = sm[at][n], M = fmaxf(m[j][e], m2), mu = M == -INFINITY ? 0.f : M;
+            const float f1 = kv8_ex2(m[j][e] - mu), f2 = kv8_ex2(m2 - mu);
+            m[j][e] = M;
+            l[j][e] = l[j][e] * f1 + sl[at][n] * f2;
+#pragma unroll
+            for (int i = 0; i < KW; ++i) {
+              o[j][i][e] = o[j][i][e] * f1 + so[(at * NQ + n) * ROW + i * 16 + c] * f2;
+              o[j][i][e + 2] = o[j][i][e + 2] * f1 + so[(at * NQ + n) * ROW + i * 16 + c + 8] * f2;
+            }
+          }
+      };
+      if (sh.tiles > 1) {   // else warp 0 has it all
+        if (warp >= 2) put(warp - 2);
+        __syncthreads();
+        if (warp < 2) take(warp);
+        __syncthreads();
+        if (warp == 1) put(1);
+        __syncthreads();
+        if (warp == 0) take(1);
+      }
+      if (warp == 0) put(0);
+      __syncthreads();
+      for (int i = threadIdx.x; i < nq * (D / 4); i += 32 * KV8_NW) {
+        const int n = i / (D / 4), d = (i % (D / 4)) * 4;
+        kv8_out<T>(p, sh.s0, h, q0 + n, d, D, *reinterpret_cast<const float4*>(so + n * ROW + d), sm[0][n], sl[0][n]);
+      }
+      return;
+    } else {
+      // ---- out, or to scratch, eight queries at a time through the stage that was read last
+      const bool all = cnt == sh.tiles;
+      const long slot = 2 * ((long)blockIdx.x * KV8_NW + warp) + (tile0 == 0);
+      float* so = reinterpret_cast<float*>(ring + (warp * 2 + (stage ^ 1)) * STAGE);   // [8][ROW]
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < KW; ++i) {
+            so[(2 * t + e) * ROW + i * 16 + c] = o[j][i][e];
+            so[(2 * t + e) * ROW + i * 16 + c + 8] = o[j][i][e + 2];
+          }
+        __syncwarp();
+        for (int i = lane; i < 8 * (D / 4); i += 32) {
+          const int n = i / (D / 4), d = (i % (D / 4)) * 4, from = n >> 1;
+          const float4 y = *reinterpret_cast<const float4*>(so + n * ROW + d);
+          const float ma = __shfl_sync(0xffffffffu, m[j][0], from), mb = __shfl_sync(0xffffffffu, m[j][1], from);
+          const float la = __shfl_sync(0xffffffffu, l[j][0], from), lb = __shfl_sync(0xffffffffu, l[j][1], from);
+          const float M = n & 1 ? mb : ma, lt = n & 1 ? lb : la;
+          if (j * 8 + n >= nq) continue;
+          if (all) {
+            kv8_out<T>(p, sh.s0, h, q0 + j * 8 + n, d, D, y, M, lt);
+          } else {
+            const long at = slot * NQ + j * 8 + n;
+            *reinterpret_cast<float4*>(p.part + at * D + d) = y;
+            if (d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(M, lt);
+          }
+        }
+      }
+      __syncwarp();
+      // ---- the next job
+      su += span;
+      x = 0;
+      cu = su + KV8_OVER;
+      if (su < R && ++job == sh.jobs) {
+        job = 0;
+        do {
+          if (++b >= p.q.B) return;   // only where lens changed meanwhile
+          sh = kv8_share<NQ, TILE>(p, b);
+        } while (sh.jobs == 0);
       }
     }
-  __syncthreads();
-  const long slot = ((long)job * L.Hkv + h) * p.S + piece;
-  for (int i = threadIdx.x; i < J.nq * (D / 4); i += 32 * KV8_NW) {
-    const int n = i / (D / 4), d = (i % (D / 4)) * 4;
-    float M = sm[0][n];
-#pragma unroll
-    for (int w = 1; w < KV8_NW; ++w) M = fmaxf(M, sm[w][n]);
-    const float mu = M == -INFINITY ? 0.f : M;
-    float lt = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < KV8_NW; ++w) {
-      const float f = kv8_ex2(sm[w][n] - mu);
-      const float4 v = *reinterpret_cast<const float4*>(&so[w][n][d]);
-      lt += sl[w][n] * f;
-      y[0] += v.x * f; y[1] += v.y * f; y[2] += v.z * f; y[3] += v.w * f;
-    }
-    if (J.pieces > 1) {
-      *reinterpret_cast<float4*>(p.part + (slot * NQ + n) * D + d) = make_float4(y[0], y[1], y[2], y[3]);
-      if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * NQ + n) * 2) = make_float2(M, lt);
-      continue;
-    }
-    const int qi = J.q0 + n, r = J.s0 + qi / G, hq = h * G + qi % G;
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
-    union { T v[4]; uint2 u; } z;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) z.v[e] = from_f<T>(y[e] * inv);
-    *reinterpret_cast<uint2*>(p.out + (long)r * p.ldo + hq * D + d) = z.u;
-    if (d == 0 && p.lse) p.lse[(long)r * p.H + hq] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * 0.6931471805599453f;
   }
 }
 
-// Merges the pieces of a (job, head): one block, NQ D / 4 columns of four
-// channels, the pieces spread over the threads that are left; sums in a fixed order.
+// Merges the jobs that runs cut.  Every warp looks at the one or two cut jobs
+// that its run has a piece of, and takes its share of each one's columns (four channels
+// of a query) over all pieces: lanes over columns, and over pieces where the
+// share has fewer columns than lanes.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(128) kv8_attn_merge_kernel(Kv8AttnP p) {
-  constexpr int NQ = 8 * NT, C4 = D / 4;
+__global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_merge_kernel(Kv8AttnP p) {
+  constexpr int NQ = 8 * NT, C4 = D / 4, TILE = Kv8Tile<D>::TILE;
+  // lengths and starts were written before the attention kernel began, which this launch follows
+  Kv8Run r;
+  const bool any = kv8_locate<NQ, TILE, false>(p, r);
   griddep_wait();
   griddep_release();
-  extern __shared__ float sw[];            // [S][NQ] weights of the pieces
-  __shared__ float4 red[128];
-  __shared__ float linv[NQ];
-  const int job = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-  Kv8Job J;
-  if (!kv8_job<NQ>(p, job, J, nullptr) || J.pieces == 1) return;
-  const long slot = ((long)job * p.L.Hkv + h) * p.S;
-  // a warp per query: its total and the weight of each piece
-  for (int n = tid >> 5; n < J.nq; n += 4) {
-    const int lane = tid & 31;
-    float M = -INFINITY, lt = 0.f;
-    for (int s = lane; s < J.pieces; s += 32) M = fmaxf(M, p.part_ml[((slot + s) * NQ + n) * 2]);
-    M = warp_max(M);
-    const float mu = M == -INFINITY ? 0.f : M;
-    for (int s = lane; s < J.pieces; s += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + ((slot + s) * NQ + n) * 2);
-      const float f = kv8_ex2(ml.x - mu);
-      sw[s * NQ + n] = f;
-      lt += ml.y * f;
+  if (!any || r.u >= r.total || r.b < 0) return;
+  const int lane = threadIdx.x & 31;
+  const long run = (long)blockIdx.x * KV8_NW + (threadIdx.x >> 5), end = min(r.u + r.quota, r.total);
+  Kv8Share sh = kv8_share<NQ, TILE>(p, r.b);
+  long j0 = r.u - r.x;   // first unit of the job
+  int b = r.b, job = r.job;
+  for (int k = 0; k < 2; ++k) {
+    if (k == 1) {
+      // the job that the run ends in
+      while (j0 + sh.tiles + KV8_OVER < end) {
+        const int w = sh.tiles + KV8_OVER;
+        const long ahead = min((end - 1 - j0) / w, (long)(sh.jobs - 1 - job));
+        if (ahead > 0) {
+          j0 += ahead * w;
+          job += (int)ahead;
+          continue;
+        }
+        j0 += w;
+        job = 0;
+        do {
+          if (++b >= p.q.B) return;
+          sh = kv8_share<NQ, TILE>(p, b);
+        } while (sh.jobs == 0);
+      }
+      if (j0 <= r.u) return;   // the first one, which is done
     }
-    lt = warp_sum(lt);
-    if (lane == 0) {
-      linv[n] = lt == 0.f ? 0.f : 1.f / lt;
-      const int qi = J.q0 + n, r = J.s0 + qi / p.G, hq = h * p.G + qi % p.G;
-      if (p.lse) p.lse[(long)r * p.H + hq] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * 0.6931471805599453f;
-    }
-  }
-  __syncthreads();
-  const int cols = J.nq * C4, groups = max(1, 128 / cols), per = min(cols, 128);
-  for (int c0 = 0; c0 < cols; c0 += 128) {
-    const int g = tid / per, col = c0 + tid % per;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool on = g < groups && col < cols;
-    const int n = col / C4, d = (col % C4) * 4;
-    if (on)
-      for (int s = g; s < J.pieces; s += groups) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part + ((slot + s) * NQ + n) * D + d);
-        const float f = sw[s * NQ + n];
+    const long t0 = j0 + KV8_OVER, t1 = t0 + sh.tiles;   // its tiles
+    if (end <= t0) return;                               // no tile of it in this run, none of a later job
+    const long w0 = t0 / r.quota, w1 = (t1 - 1) / r.quota;
+    const int pieces = (int)(w1 - w0) + 1;
+    if (pieces == 1) continue;
+    const int h = job % p.L.Hkv, q0 = job / p.L.Hkv * NQ, nq = min(NQ, sh.n * p.G - q0), cols = nq * C4;
+    const int share = (cols + pieces - 1) / pieces, c0 = (int)(run - w0) * share, c1 = min(cols, c0 + share);
+    auto slot = [&](int s) -> long { return 2 * (w0 + s) + (s == 0); };
+    int wide = 1;
+    while (wide < 32 && wide < c1 - c0) wide <<= 1;
+    for (int cb = c0; cb < c1; cb += wide) {
+      const int col = cb + (lane & (wide - 1)), n = min(col, c1 - 1) / C4, d = (min(col, c1 - 1) % C4) * 4;
+      const int lanes = 32 / wide;
+      float M = -INFINITY, lt = 0.f;
+      for (int s = lane / wide; s < pieces; s += lanes) M = fmaxf(M, p.part_ml[(slot(s) * NQ + n) * 2]);
+      for (int o = wide; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float mu = M == -INFINITY ? 0.f : M;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int s = lane / wide; s < pieces; s += lanes) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot(s) * NQ + n) * 2);
+        const float4 v = *reinterpret_cast<const float4*>(p.part + (slot(s) * NQ + n) * D + d);
+        const float f = kv8_ex2(ml.x - mu);
+        lt += ml.y * f;
         y.x += v.x * f; y.y += v.y * f; y.z += v.z * f; y.w += v.w * f;
       }
-    if (groups > 1) {
-      red[tid] = y;
-      __syncthreads();
-      if (g == 0)
-        for (int k = 1; k < groups; ++k) {
-          const float4 v = red[k * per + tid];
-          y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
-        }
-    }
-    if (on && g == 0) {
-      const int qi = J.q0 + n, r = J.s0 + qi / p.G, hq = h * p.G + qi % p.G;
-      const float inv = linv[n];
-      union { T v[4]; uint2 u; } z;
-      z.v[0] = from_f<T>(y.x * inv); z.v[1] = from_f<T>(y.y * inv);
-      z.v[2] = from_f<T>(y.z * inv); z.v[3] = from_f<T>(y.w * inv);
-      *reinterpret_cast<uint2*>(p.out + (long)r * p.ldo + hq * D + d) = z.u;
+      for (int o = wide; o < 32; o <<= 1) {
+        lt += __shfl_xor_sync(0xffffffffu, lt, o);
+        y.x += __shfl_xor_sync(0xffffffffu, y.x, o); y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
+        y.z += __shfl_xor_sync(0xffffffffu, y.z, o); y.w += __shfl_xor_sync(0xffffffffu, y.w, o);
+      }
+      if (lane < wide && col < c1) kv8_out<T>(p, sh.s0, h, q0 + n, d, D, y, M, lt);
     }
   }
 }
@@ -762,61 +1069,80 @@ static cudaError_t append_t(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 gr
 }
 
 struct Kv8Plan {
-  int nt, jobs, S;
+  int nt, blocks, whole;
   size_t part, ml;   // floats
 };
-// Queries a tile: 8, 16 or 32 (16 at most for 128 channels, whose sums fill
-// the registers), by the mean number of queries a sequence; more of them read
-// the cache fewer times, fewer waste less of the products.  Pieces: as many
-// as give every SM three blocks or so of a quarter of a wave each, no more than
-// the longest row has tiles for.
+// Queries a job: 8, 16 or 32 (16 at most for 128 channels, whose sums fill the
+// registers), by the mean number of queries a sequence; more of them read the
+// cache fewer times, fewer waste less of the products.  Blocks: as many as are
+// resident at once (three an SM by shared memory; two where the sums take 255
+// registers), or one per job where no job has more than KV8_WHOLE tiles.
 static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
   static int sms = 0;
   if (!sms) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
+      sms = n;
+    else
       cudaGetLastError();
-      sms = 148;
-    }
   }
   Kv8Plan P;
-  const int G = H / c.n_kv_heads;
+  const int G = H / c.n_kv_heads, tile = c.head_dim == 128 ? 32 : 64;
   const long per = b.B ? ((long)b.rows + b.B - 1) / b.B * G : G;
   P.nt = per <= 8 ? 1 : per <= 16 || c.head_dim == 128 ? 2 : 4;
   const int nq = 8 * P.nt;
-  P.jobs = b.start ? (int)((long)b.rows * G / nq) + b.B : b.B * ((G + nq - 1) / nq);
-  const long base = (long)P.jobs * c.n_kv_heads, tiles = ((long)b.max_pages * c.page + 63) / 64;
-  const long want = base ? (12L * sms + base - 1) / base : 1;
-  P.S = (int)std::max(1L, std::min(std::min(want, 128L), (tiles + KV8_MINT - 1) / KV8_MINT));
-  const size_t n = P.S > 1 ? (size_t)base * P.S * nq : 0;
-  P.part = n * c.head_dim;
-  P.ml = n * 2;
+  const long jobs = (b.start ? (long)b.rows * G / nq + b.B : (long)b.B * ((G + nq - 1) / nq)) * c.n_kv_heads;
+  const long tiles = ((long)b.max_pages * c.page + tile - 1) / tile;
+  P.whole = tiles <= KV8_WHOLE;
+  const long resident = (P.nt == 4 || (P.nt == 2 && c.head_dim == 128) ? 2L : 3L) * (sms ? sms : 148);
+  P.blocks = (int)(P.whole ? jobs : std::min(resident, (jobs * tiles + KV8_NW - 1) / KV8_NW));
+  P.part = P.whole ? 0 : (size_t)P.blocks * KV8_NW * 2 * nq * c.head_dim;
+  P.ml = P.whole ? 0 : (size_t)P.blocks * KV8_NW * 2 * nq * 2;
   return P;
 }
 
+template <typename T, int D, int NT, int KIND, bool WHOLE>
+static cudaError_t attn_launch(const Kv8AttnP& p, const Kv8Plan& P, cudaStream_t s) {
+  constexpr size_t smem = kv8_attn_smem<D, NT, WHOLE>();
+  if (smem > 48000) {
+    static bool ready[64] = {};   // per device: the attribute is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !ready[dev]) {
+      e = cudaFuncSetAttribute(kv8_attn_kernel<T, D, NT, KIND, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)smem);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) ready[dev] = true;
+    }
+  }
+  ++g_kernel_launches;
+  return launch_k(kv8_attn_kernel<T, D, NT, KIND, WHOLE>, dim3(P.blocks), dim3(32 * KV8_NW), smem, s, p);
+}
 template <typename T, int D, int NT, int KIND>
-static cudaError_t attn_nt(const Kv8AttnP& p, const Kv8Plan& P, int Hkv, cudaStream_t s) {
-  cudaError_t e = launch_k(kv8_attn_kernel<T, D, NT, KIND>, dim3((unsigned)P.jobs * P.S, Hkv), dim3(32 * KV8_NW), 0, s, p);
+static cudaError_t attn_nt(const Kv8AttnP& p, const Kv8Plan& P, cudaStream_t s) {
+  if (P.whole) return attn_launch<T, D, NT, KIND, true>(p, P, s);
+  const cudaError_t e = attn_launch<T, D, NT, KIND, false>(p, P, s);
+  if (e != cudaSuccess) return e;
   ++g_kernel_launches;
-  if (e != cudaSuccess || P.S == 1) return e;
-  ++g_kernel_launches;
-  return launch_k(kv8_attn_merge_kernel<T, D, NT>, dim3(P.jobs, Hkv), dim3(128), (size_t)P.S * 8 * NT * 4, s, p);
+  return launch_k(kv8_attn_merge_kernel<T, D, NT>, dim3(P.blocks), dim3(32 * KV8_NW), 0, s, p);
 }
 template <typename T, int D, int KIND>
-static cudaError_t attn_d(const Kv8AttnP& p, const Kv8Plan& P, int Hkv, cudaStream_t s) {
-  if (P.nt == 1) return attn_nt<T, D, 1, KIND>(p, P, Hkv, s);
+static cudaError_t attn_d(const Kv8AttnP& p, const Kv8Plan& P, cudaStream_t s) {
+  if (P.nt == 1) return attn_nt<T, D, 1, KIND>(p, P, s);
   if constexpr (D < 128) {
-    if (P.nt == 4) return attn_nt<T, D, 4, KIND>(p, P, Hkv, s);
+    if (P.nt == 4) return attn_nt<T, D, 4, KIND>(p, P, s);
   }
-  return attn_nt<T, D, 2, KIND>(p, P, Hkv, s);
+  return attn_nt<T, D, 2, KIND>(p, P, s);
 }
 template <typename T, int KIND>
-static cudaError_t attn_t(const Kv8AttnP& p, const Kv8Plan& P, const gpt_kv8_cache& c, cudaStream_t s) {
-  switch (c.head_dim) {
-    case 16: return attn_d<T, 16, KIND>(p, P, c.n_kv_heads, s);
-    case 32: return attn_d<T, 32, KIND>(p, P, c.n_kv_heads, s);
-    case 64: return attn_d<T, 64, KIND>(p, P, c.n_kv_heads, s);
-    default: return attn_d<T, 128, KIND>(p, P, c.n_kv_heads, s);
+static cudaError_t attn_t(const Kv8AttnP& p, const Kv8Plan& P, int D, cudaStream_t s) {
+  switch (D) {
+    case 16: return attn_d<T, 16, KIND>(p, P, s);
+    case 32: return attn_d<T, 32, KIND>(p, P, s);
+    case 64: return attn_d<T, 64, KIND>(p, P, s);
+    default: return attn_d<T, 128, KIND>(p, P, s);
   }
 }
 
@@ -887,17 +1213,17 @@ int gpt_kv8_attention(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b,
   if (*why) return kv8_refuse("gpt_kv8_attention", why);
   if (b->B == 0 || b->rows == 0) return GPT_OK;
   const Kv8Plan P = kv8_plan(*c, *b, n_heads);
-  if ((long)P.jobs * P.S > 0x7fffffffL) return kv8_refuse("gpt_kv8_attention", "too many queries");
-  if (P.S > 1 && (!work || work_bytes < (P.part + P.ml) * sizeof(float) || ((uintptr_t)work & 15)))
+  if (!P.whole && (!work || work_bytes < (P.part + P.ml) * sizeof(float) || ((uintptr_t)work & 15)))
     return kv8_refuse("gpt_kv8_attention", "work must be 16-byte aligned and hold gpt_kv8_attention_work bytes");
   Kv8AttnP p = {kv8_layer(*c, layer), kv8_seqs(*b), (const uint16_t*)q, (uint16_t*)out, lse, ldq, ldo,
-                n_heads, n_heads / c->n_kv_heads, P.S, scale, (float*)work, (float*)work + P.part, err};
+                n_heads, n_heads / c->n_kv_heads, b->max_pages * c->page, scale, (float*)work, (float*)work + P.part, err};
   cudaStream_t s = (cudaStream_t)stream;
   const bool i8 = c->kind == GPT_KV8_INT8;
+  const int D = c->head_dim;
   return kv8_done("gpt_kv8_attention",
                   dtype == GPT_PRECISION_BF16
-                      ? (i8 ? attn_t<bf16, GPT_KV8_INT8>(p, P, *c, s) : attn_t<bf16, GPT_KV8_E4M3>(p, P, *c, s))
-                      : (i8 ? attn_t<f16, GPT_KV8_INT8>(p, P, *c, s) : attn_t<f16, GPT_KV8_E4M3>(p, P, *c, s)));
+                      ? (i8 ? attn_t<bf16, GPT_KV8_INT8>(p, P, D, s) : attn_t<bf16, GPT_KV8_E4M3>(p, P, D, s))
+                      : (i8 ? attn_t<f16, GPT_KV8_INT8>(p, P, D, s) : attn_t<f16, GPT_KV8_E4M3>(p, P, D, s)));
 }
 
 }  // extern "C"
