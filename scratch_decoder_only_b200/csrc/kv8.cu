@@ -274,13 +274,14 @@ __global__ void __launch_bounds__(128) kv8_read_kernel(Kv8ReadP p) {
 // brought up to date only when a score passes it by 2^8 (w <= 256 in f16), so
 // most tiles need no reduction over lanes and no rescaling.
 //
-// Latency: the codes of a warp's next tile travel by asynchronous copies into
-// shared memory while it works on the present one; the page ids of the tile
-// after that are being loaded.  Lanes copy whole 128-byte lines (an
-// asynchronous copy whose eight lanes lie in different lines is taken apart lane by
-// lane) to places permuted so that the reads above have no bank conflicts.
-// Three blocks of four warps an SM keep about 100 KB in flight; warps meet no
-// barrier while they run.
+// Latency: a tile's values travel by asynchronous copies into shared memory
+// while the warp works on its keys, the next tile's keys while it works on the
+// weights and values; the page ids of the tile after that are being loaded.  One
+// buffer of 4 KB each is enough for that, so registers, not shared memory, set
+// the number of warps (16 an SM with eight queries), and a warp meets no
+// barrier while it runs.  Lanes copy whole 128-byte lines (an asynchronous copy
+// whose eight lanes lie in different lines is taken apart lane by lane) to places
+// permuted so that the reads above have no bank conflicts.
 //
 // Rounding: q is taken to f16 with a power of two of its own per query, which
 // keeps all of bf16's bits down to 2^-28 of the query's largest element (fp16
@@ -313,7 +314,14 @@ struct Kv8AttnP {
   int H, G, cap;
   float scale;
   float *part, *part_ml;   // [run][2][NQ][D] sums, [run][2][NQ][2] (m, l)
+  struct Kv8Piece* piece;  // [run][2]
   unsigned* err;
+};
+
+// A partial result of a run: its job is cut into `pieces` (0: there is none), the
+// first of them from run w0; the job's first row, query, queries, head.
+struct __align__(16) Kv8Piece {
+  int pieces, w0, s0, q0, nq, h, pad[2];
 };
 
 __device__ __forceinline__ float kv8_ex2(float x) {
@@ -333,14 +341,8 @@ __device__ __forceinline__ uint32_t kv8_transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-// N bytes, or N zeros
-template <int N>
-__device__ __forceinline__ void kv8_copy(uint32_t dst, const uint8_t* src, bool on) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(on ? N : 0), "n"(N)
-                 : "memory");
+__device__ __forceinline__ void kv8_copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void kv8_lds(uint32_t* r, uint32_t src) {
@@ -377,18 +379,27 @@ __device__ __forceinline__ Kv8Share kv8_share(const Kv8AttnP& p, int b) {
 }
 
 // Where this warp's run begins (WHOLE: where the block's job is): the sequence,
-// its job, the unit in the job.  Run number blockIdx.x * KV8_NW + warp covers
-// units [run * quota, (run + 1) * quota) of total.  All threads of the block call
+// its job, the unit in the job.  Run number run0 + warp of `runs` covers units
+// [run * quota, (run + 1) * quota) of total.  All threads of the block call
 // this; false: no such run.
 struct Kv8Run {
   int b, job, x;
   long u, quota, total;
 };
 template <int NQ, int TILE, bool WHOLE>
-__device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, Kv8Run& r) {
+__device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, long runs, long run0, Kv8Run& r) {
   __shared__ long wsum[KV8_NW], sh_rem[KV8_NW];
   __shared__ int sh_b[KV8_NW];
+  constexpr int PER = WHOLE ? 1 : KV8_NW;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.q.B;
+  if (WHOLE && !p.q.start) {
+    // the same jobs for each sequence
+    const int per = (p.G + NQ - 1) / NQ * p.L.Hkv;
+    r.b = (int)(run0 / per);
+    r.job = (int)(run0 % per);
+    r.x = KV8_OVER;
+    return r.b < B;
+  }
   auto units = [&](int b) -> long {
     if (b >= B) return 0;
     const Kv8Share s = kv8_share<NQ, TILE>(p, b);
@@ -397,7 +408,7 @@ __device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, Kv8Run& r) {
   const long mine = units(tid);   // of the first 128 sequences
   r.total = 0;
   r.quota = 1;
-  long u0 = blockIdx.x;
+  long u0 = run0;
   if (!WHOLE) {
     long sum = mine;
     for (int b = tid + 32 * KV8_NW; b < B; b += 32 * KV8_NW) sum += units(b);
@@ -406,14 +417,14 @@ __device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, Kv8Run& r) {
     if (lane == 0) wsum[warp] = sum;
     __syncthreads();
     for (int w = 0; w < KV8_NW; ++w) r.total += wsum[w];
-    const long runs = (long)gridDim.x * KV8_NW;
     r.quota = max((long)KV8_OVER + 1, (r.total + runs - 1) / runs);
-    u0 = (long)blockIdx.x * KV8_NW * r.quota;
+    u0 = run0 * r.quota;
     if (u0 >= r.total) return false;
-    if (tid < KV8_NW) sh_b[tid] = -1;
+    if (tid < PER) sh_b[tid] = -1;
   }
-  r.u = WHOLE ? u0 : u0 + warp * r.quota;
-  const long u3 = WHOLE ? u0 : min(u0 + (KV8_NW - 1) * r.quota, r.total - 1);
+  const int ask = PER == 1 ? 0 : warp;
+  r.u = u0 + ask * r.quota;
+  const long u3 = WHOLE ? u0 : min(u0 + (PER - 1) * r.quota, r.total - 1);
   long carry = 0;
   for (int b0 = 0; b0 < B; b0 += 32 * KV8_NW) {
     const long v = b0 ? units(b0 + tid) : mine;
@@ -431,7 +442,7 @@ __device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, Kv8Run& r) {
       if (w < warp) first += wsum[w];
       carry += wsum[w];
     }
-    for (int w = 0; w < (WHOLE ? 1 : KV8_NW); ++w) {
+    for (int w = 0; w < PER; ++w) {
       const long u = u0 + w * r.quota;
       if (u >= first && u < first + v) {
         sh_b[w] = b0 + tid;
@@ -442,8 +453,8 @@ __device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, Kv8Run& r) {
   }
   if (WHOLE && carry <= u0) return false;
   __syncthreads();
-  r.b = sh_b[WHOLE ? 0 : warp];
-  const long rem = sh_rem[WHOLE ? 0 : warp];
+  r.b = sh_b[ask];
+  const long rem = sh_rem[ask];
   if (WHOLE) {
     r.job = (int)rem;
     r.x = KV8_OVER;
@@ -458,12 +469,14 @@ __device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, Kv8Run& r) {
 template <int D>
 struct Kv8Tile {
   static constexpr int TILE = D == 128 ? 32 : 64;
-  static constexpr int STAGE = TILE * D * 2;   // bytes a warp copies at a time
+  static constexpr int HALF = TILE * D;   // bytes of a tile's keys, and of its values
 };
 template <int D, int NT, bool WHOLE>
 constexpr size_t kv8_attn_smem() {
-  return (size_t)KV8_NW * 2 * Kv8Tile<D>::STAGE + (WHOLE ? (size_t)2 * 8 * NT * (D + 4) * 4 : 0);
+  return (size_t)KV8_NW * 2 * Kv8Tile<D>::HALF + (WHOLE ? (size_t)2 * 8 * NT * (D + 4) * 4 : 0);
 }
+// Blocks an SM holds: what their registers allow (128, 168 and 255 a thread).
+__host__ __device__ constexpr int kv8_resident(int D, int nt) { return nt == 1 ? 4 : nt == 2 && D < 128 ? 3 : 2; }
 
 // The result of query q0 + n of a job, four channels from d on.
 template <typename T>
@@ -479,8 +492,8 @@ __device__ __forceinline__ void kv8_out(const Kv8AttnP& p, int s0, int h, int qi
 }
 
 template <typename T, int D, int NT, int KIND, bool WHOLE>
-__global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
-  constexpr int NQ = 8 * NT, KW = D / 16, ROW = D + 4, TILE = Kv8Tile<D>::TILE, STAGE = Kv8Tile<D>::STAGE;
+__global__ void __launch_bounds__(32 * KV8_NW, kv8_resident(D, NT)) kv8_attn_kernel(Kv8AttnP p) {
+  constexpr int NQ = 8 * NT, KW = D / 16, TILE = Kv8Tile<D>::TILE, HALF = Kv8Tile<D>::HALF;
   constexpr int TQ = TILE / 4;                         // tokens of a quarter
   constexpr int KP = D / 4 < 16 ? D / 4 : 16, KT = D / 4 / KP;   // bytes of a key read, reads of a quarter key
   constexpr int STEP = WHOLE ? KV8_NW : 1;
@@ -490,7 +503,6 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
   const Kv8Layer& L = p.L;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane >> 2, t = lane & 3;
   const int G = p.G, lp = L.lp, pmask = (1 << lp) - 1, Hkv = L.Hkv;
-  const long pd = (long)D << lp;
   if (blockIdx.x == 0) {
     for (int b = threadIdx.x; b < p.q.B; b += 32 * KV8_NW) {
       if (p.q.start && (p.q.start[b] < 0 || p.q.start[b + 1] < p.q.start[b] || p.q.start[b + 1] > p.q.rows))
@@ -500,29 +512,31 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
     }
   }
   Kv8Run r;
-  if (!kv8_locate<NQ, TILE, WHOLE>(p, r)) return;
+  const long run = (long)blockIdx.x * KV8_NW + warp;
+  if (!WHOLE && lane < 2) p.piece[2 * run + lane].pieces = 0;
+  if (!kv8_locate<NQ, TILE, WHOLE>(p, (long)gridDim.x * KV8_NW, (long)blockIdx.x * (WHOLE ? 1 : KV8_NW), r)) return;
   if (!WHOLE && (r.u >= r.total || r.b < 0)) return;   // no barrier follows
   Kv8Share sh = kv8_share<NQ, TILE>(p, r.b);
   // units of this run, counted from its begin; a job's first KV8_OVER have no tile
   const int R = WHOLE ? sh.tiles : (int)min(r.quota, r.total - r.u);
 
-  // ---- the warp's next tile: sequence nb, head nh, tile nt of nm, the job's number nj of njobs; the page of
-  // this lane's quarter (-1: none); nu: the unit
+  // ---- the warp's next tile: sequence nb, head nh, tile nt of nm, the job's number nj of njobs; nu: the unit; the
+  // page-and-head number of this lane's quarter (none: KV8_NONE)
+  constexpr uint32_t KV8_NONE = 0xffffffffu;
   int nb = r.b, nj = r.job, nh = r.job % Hkv, nt = r.x - KV8_OVER, nm = sh.tiles, njobs = sh.jobs;
-  int nlen = min(max(sh.len, 0), p.cap), nid = -1, nu = 0;
+  int nlen = min(max(sh.len, 0), p.cap), nu = 0;
+  uint32_t nph = KV8_NONE;
   if (nt < 0) {
     nu = -nt;
     nt = 0;
   }
   auto page = [&]() {
     const int tok = nt * TILE + TQ * t;
-    nid = -1;
+    nph = KV8_NONE;
     if (nu < R && tok < nlen) {
-      nid = p.q.table[(long)nb * p.q.ld_table + (tok >> lp)];
-      if ((unsigned)nid >= (unsigned)L.n_pages) {
-        set_dev_err(p.err, GPT_DEVERR_PAGE);
-        nid = -1;
-      }
+      const uint32_t id = p.q.table[(long)nb * p.q.ld_table + (tok >> lp)];
+      if (id < (uint32_t)L.n_pages) nph = id * Hkv + nh;
+      else set_dev_err(p.err, GPT_DEVERR_PAGE);
     }
   };
   auto advance = [&]() {
@@ -551,50 +565,49 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
     }
     page();
   };
-  const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + warp * 2 * STAGE;
+  const uint32_t kbuf = (uint32_t)__cvta_generic_to_shared(ring) + warp * 2 * HALF, vbuf = kbuf + HALF;
   float ks_next = 0.f, vs_next = 0.f;
-  int id_next = -1;
-  // Keys lie in a stage token by token, values by group of 16 tokens and
+  bool kon_next = false, von_next = false;   // the key's quarter, the value's has a page
+  unsigned has = 0;                          // bit t: quarter t has one
+  uint32_t place = 0;
+  // Keys lie in their buffer token by token, values by group of 16 tokens and
   // channel, 16 bytes a piece.  Bits 4 to 6 of the address are exchanged by
-  // exclusive or within a 128-byte line so that the eight lanes of a 16-byte read (16 of an
-  // 8-byte, 32 of a 4-byte one) meet eight (16, 32) different bank groups.
-  auto fetch = [&](int stage) {
-    if (nu < R) {
-      const int tb = nt * TILE;
-      const uint32_t s0 = ring0 + stage * STAGE;
+  // exclusive or within a 128-byte line so that the eight lanes of a 16-byte
+  // read (16 of an 8-byte, 32 of a 4-byte one) meet different bank groups.
+  // Both have the same place in k and in v, here in units of 16 bytes, which
+  // 32 bits hold for 64 GB a layer.
+  auto copy = [&](uint32_t buf, const uint8_t* from, bool keys) {
 #pragma unroll
-      for (int g = 0; g < TILE / 16; ++g) {
-        // group g of the tile: 16 tokens of one page
-        const int id = __shfl_sync(0xffffffffu, nid, g * (16 / TQ));
-        const size_t ph = (size_t)max(id, 0) * Hkv + nh;
-        const long at = ph * pd + ((tb + 16 * g) & pmask) * D + lane * 16;
-        const bool on = id >= 0;
-        constexpr int N = D / 32 ? D / 32 : 1;   // copies of 32 lanes a group
-        const bool mine = D >= 32 || lane < 16;
-        const uint32_t kx = D == 128 ? (lane >> 3 & 1) << 6 : D == 64 ? 0 : (g & (64 / D - 1)) * 2 * D;
-        const uint32_t vx = TQ == 16 ? (g & 3) << 5 : (g & 1) << 6;
+    for (int g = 0; g < TILE / 16; ++g) {
+      const uint32_t at = __shfl_sync(0xffffffffu, place, g * (16 / TQ));
+      constexpr int N = D / 32 ? D / 32 : 1;   // copies of 32 lanes a group
+      const uint32_t kx = D == 128 ? (lane >> 3 & 1) << 6 : D == 64 ? 0 : (g & (64 / D - 1)) * 2 * D;
+      const uint32_t vx = TQ == 16 ? (g & 3) << 5 : (g & 1) << 6;
+      if (has >> g * (16 / TQ) & 1 && (D >= 32 || lane < 16)) {
+        const uint8_t* a = from + (size_t)at * 16;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (mine) {
-            kv8_copy<16>(s0 + g * 16 * D + i * 512 + (lane * 16 ^ kx), L.k + at + i * 512, on);
-            kv8_copy<16>(s0 + TILE * D + g * 16 * D + i * 512 + (lane * 16 ^ vx), L.v + at + i * 512, on);
-          }
-        }
+        for (int i = 0; i < N; ++i) kv8_copy16(buf + g * 16 * D + i * 512 + (lane * 16 ^ (keys ? kx : vx)), a + i * 512);
       }
-      const int idk = __shfl_sync(0xffffffffu, nid, c >> 1);
-      const size_t phk = (size_t)max(idk, 0) * Hkv + nh;
-      ks_next = idk >= 0 ? L.ks[phk] : 0.f;
-      vs_next = idk >= 0 ? L.vs[phk] : 0.f;
     }
-    id_next = nid;
     asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto fetch_keys = [&]() {
+    // of this lane's quarter: its 16-token group (the token's slot rounded down)
+    place = nph * (uint32_t)(D / 16 << lp) + ((nt * TILE + TQ * t) & pmask & ~15) * (D / 16);
+    has = __ballot_sync(0xffffffffu, nph != KV8_NONE) & 15u;
+    copy(kbuf, L.k + lane * 16, true);
+    const uint32_t ph = __shfl_sync(0xffffffffu, nph, c >> 1);
+    kon_next = ph != KV8_NONE;
+    von_next = nph != KV8_NONE;
+    ks_next = kon_next ? L.ks[ph] : 0.f;
+    vs_next = kon_next ? L.vs[ph] : 0.f;
   };
   if (WHOLE) {
     nu += warp;
     nt += warp;
   }
   page();
-  fetch(0);
+  fetch_keys();
   advance();
 
   // ---- this lane's read offsets in a stage
@@ -607,9 +620,9 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
     else koff = tk * D + t * (D / 4);
     if constexpr (D < 64) koff ^= (tk >> 4 & (64 / D - 1)) * 2 * D;
     const int g = t * TQ >> 4;
-    voff = TILE * D + g * 16 * D + (c * 16 ^ (TQ == 16 ? g << 5 : g << 6)) + (t * TQ & 15);
+    voff = g * 16 * D + (c * 16 ^ (TQ == 16 ? g << 5 : g << 6)) + (t * TQ & 15);
   }
-  int stage = 0, cu = WHOLE ? warp : max(0, KV8_OVER - r.x);
+  int cu = WHOLE ? warp : max(0, KV8_OVER - r.x);
   int b = r.b, job = r.job, x = r.x;
   for (int su = 0; su < R;) {
     // ---- one job of the run: units [su, su + span), tiles [tile0, tile0 + cnt)
@@ -654,7 +667,8 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
         up = __int_as_float(max(1, min(254, 258 - max(ex, 1))) << 23);
       }
       bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 28) & 15u) != 0;   // of the query's four lanes
-      const float fac = bad ? NAN : p.scale * 1.4426950408889634f * (1.f / up);
+      const float fac = bad ? NAN : fabsf(p.scale) * 1.4426950408889634f * (1.f / up);
+      if (p.scale < 0.f) up = -up;   // the factors are not negative
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
 #pragma unroll
@@ -687,17 +701,14 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
     }
 
     for (; cu < su + span; cu += STEP) {
-      const int id = id_next;
       const float ks = ks_next, vs = vs_next;
-      __syncwarp();   // the stage of the tile before has been read by all lanes
-      fetch(stage ^ 1);
-      advance();
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      const bool kon = kon_next, von = von_next, on = has == 15u;
+      __syncwarp();   // the values of the tile before have been read by all lanes
+      copy(vbuf, L.v + lane * 16, false);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");   // the keys
       __syncwarp();
-      const uint32_t s0 = ring0 + stage * STAGE;
-      stage ^= 1;
       const int tb = (tile0 + cu - su - skip) * TILE, gv = tb + TQ * t, gk = tb + TQ * (c >> 1);
-      const bool full = !__any_sync(0xffffffffu, id < 0) && tb + TILE <= minlim;
+      const bool full = on && tb + TILE <= minlim;
       // ---- scores^T: s[i][j][e + 2 r] is token gk + (c & 1) + 4 i + 2 r with query 8 j + 2 t + e
       float s[TQ / 4][NT][4];
 #pragma unroll
@@ -708,7 +719,7 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
 #pragma unroll
           for (int w = 0; w < KT; ++w) {
             const uint32_t at = w ? koff ^ 64 : koff, more = (4 * i + 2 * e) * D;
-            kv8_lds<KP>(&kr[e][w * 4], s0 + (D < 64 ? at ^ more : at + more));
+            kv8_lds<KP>(&kr[e][w * 4], kbuf + (D < 64 ? at ^ more : at + more));
           }
 #pragma unroll
         for (int j = 0; j < NT; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.f;
@@ -721,87 +732,96 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
           for (int j = 0; j < NT; ++j) kv8_mma(s[i][j], a, qf[j][w]);
         }
       }
+      __syncwarp();   // all lanes have read the keys
+      fetch_keys();
+      advance();
+      // ---- weights; a tile that some query sees in part takes the form with comparisons
       float fac[NT][2];
-      bool stale = !full || vs > vref;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          fac[j][e] = cq[j][e] * ks;
-          float mx = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < TQ / 2; ++i) mx = fmaxf(mx, fmaf(s[i >> 1][j][e + 2 * (i & 1)], fac[j][e], -m[j][e]));
-          stale |= mx > 8.f;
-        }
-      const bool kon = __shfl_sync(0xffffffffu, id, c >> 1) >= 0;
-      if (__any_sync(0xffffffffu, stale)) {
-        float tv = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 8));
-        tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 16));
-        const float vnew = fmaxf(vref, tv);
-        vinv = vnew > 0.f ? 1.f / vnew : 1.f;   // (all scales 0, or NaN: they stay what they are)
-        const float vold = vnew > 0.f ? vref * vinv : 1.f;
-        vref = vnew;
+      uint32_t wf[TQ / 4][NT][2];
+      auto weigh = [&](auto part) {
+        constexpr bool PART = decltype(part)::value;
+        auto seen = [&](int i, int j, int e) { return !PART || (gk + (c & 1) + 2 * i < lim[j][e] && kon); };
+        bool stale = PART || vs > vref;
+        float top[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < TQ / 2; ++i) {
-              const float y = s[i >> 1][j][e + 2 * (i & 1)] * fac[j][e];
-              if (full || (gk + (c & 1) + 2 * i < lim[j][e] && kon)) mx = fmaxf(mx, y);
-            }
-#pragma unroll
-            for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-            const float mn = fmaxf(m[j][e], mx), al = kv8_ex2(m[j][e] - (mn == -INFINITY ? 0.f : mn));
-            m[j][e] = mn;
-            l[j][e] *= al;
-#pragma unroll
-            for (int i = 0; i < KW; ++i) {
-              o[j][i][e] *= al * vold;
-              o[j][i][e + 2] *= al * vold;
-            }
+            for (int i = 0; i < TQ / 2; ++i)
+              if (seen(i, j, e)) mx = fmaxf(mx, s[i >> 1][j][e + 2 * (i & 1)]);
+            top[j][e] = mx * fac[j][e];   // (-inf * 0 and a NaN scale: NaN, which no maximum takes)
+            stale |= top[j][e] > m[j][e] + 8.f;
           }
-      }
-      const float vfac = vs * vinv;
-      uint32_t wf[TQ / 4][NT][2];
+        if (__any_sync(0xffffffffu, stale)) {
+          float tv = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 8));
+          tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 16));
+          const float vnew = fmaxf(vref, tv);
+          vinv = vnew > 0.f ? 1.f / vnew : 1.f;   // (all scales 0, or NaN: they stay what they are)
+          const float vold = vnew > 0.f ? vref * vinv : 1.f;
+          vref = vnew;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+          for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mu = m[j][e] == -INFINITY ? 0.f : m[j][e];
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(-INFINITY, top[j][e]);
 #pragma unroll
-          for (int i = 0; i < TQ / 2; ++i) {
-            float& y = s[i >> 1][j][e + 2 * (i & 1)];
-            const float w = kv8_ex2(fmaf(y, fac[j][e], -mu));
-            // a token that is not seen weighs 0 even where its page's scale is NaN
-            if (full || (gk + (c & 1) + 2 * i < lim[j][e] && kon)) {
-              l[j][e] += w;
-              y = w * vfac;
-            } else {
-              y = 0.f;
+              for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+              const float mn = fmaxf(m[j][e], mx), al = kv8_ex2(m[j][e] - (mn == -INFINITY ? 0.f : mn));
+              m[j][e] = mn;
+              l[j][e] *= al;
+#pragma unroll
+              for (int i = 0; i < KW; ++i) {
+                o[j][i][e] *= al * vold;
+                o[j][i][e + 2] *= al * vold;
+              }
             }
-          }
         }
+        const float vfac = vs * vinv;
 #pragma unroll
-        for (int i = 0; i < TQ / 4; ++i)
+        for (int j = 0; j < NT; ++j) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const __half2 w = __floats2half2_rn(s[i][j][2 * e], s[i][j][2 * e + 1]);
-            wf[i][j][e] = kv8_transpose8(*reinterpret_cast<const uint32_t*>(&w));
+            const float mu = m[j][e] == -INFINITY ? 0.f : m[j][e];
+#pragma unroll
+            for (int i = 0; i < TQ / 2; ++i) {
+              float& y = s[i >> 1][j][e + 2 * (i & 1)];
+              const float w = kv8_ex2(fmaf(y, fac[j][e], -mu));
+              // a token that is not seen weighs 0 even where its page's scale is NaN
+              l[j][e] += seen(i, j, e) ? w : 0.f;
+              y = seen(i, j, e) ? w * vfac : 0.f;
+            }
           }
+#pragma unroll
+          for (int i = 0; i < TQ / 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const __half2 w = __floats2half2_rn(s[i][j][2 * e], s[i][j][2 * e + 1]);
+              wf[i][j][e] = kv8_transpose8(*reinterpret_cast<const uint32_t*>(&w));
+            }
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        fac[j][0] = cq[j][0] * ks;
+        fac[j][1] = cq[j][1] * ks;
       }
+      if (full) weigh(std::false_type{});
+      else weigh(std::true_type{});
       // ---- out^T += V^T W^T
+      asm volatile("cp.async.wait_group 1;" ::: "memory");   // the values
+      __syncwarp();
 #pragma unroll
       for (int k = 0; k < KW; ++k) {
         uint32_t vr[2][TQ / 4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          kv8_lds<TQ>(vr[e], s0 + voff + (2 * k + e) * 128);
+          kv8_lds<TQ>(vr[e], vbuf + voff + (2 * k + e) * 128);
           if (!full) {
             // unwritten slots may hold any byte, also e4m3's NaN: 0 * NaN must not reach the sums
 #pragma unroll
-            for (int w = 0; w < TQ / 4; ++w) vr[e][w] = kv8_low_bytes(vr[e][w], slen - gv - 4 * w);
+            for (int w = 0; w < TQ / 4; ++w) vr[e][w] = von ? kv8_low_bytes(vr[e][w], slen - gv - 4 * w) : 0u;
           }
         }
 #pragma unroll
@@ -829,7 +849,8 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
       }
     if constexpr (WHOLE) {
       // ---- merge the warps: 2, 3 into 0, 1, then 1 into 0, whose result goes out
-      float* so = reinterpret_cast<float*>(ring + KV8_NW * 2 * STAGE);   // [2][NQ][ROW]
+      constexpr int ROW = D + 4;
+      float* so = reinterpret_cast<float*>(ring + KV8_NW * 2 * HALF);   // [2][NQ][ROW]
       __shared__ float sm[2][NQ], sl[2][NQ];
       auto put = [&](int at) {
 #pragma unroll
@@ -882,10 +903,17 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
       }
       return;
     } else {
-      // ---- out, or to scratch, eight queries at a time through the stage that was read last
+      // ---- out, or to scratch, eight queries at a time through the values' buffer
+      constexpr int ROW = D == 128 ? D : D + 4;
       const bool all = cnt == sh.tiles;
-      const long slot = 2 * ((long)blockIdx.x * KV8_NW + warp) + (tile0 == 0);
-      float* so = reinterpret_cast<float*>(ring + (warp * 2 + (stage ^ 1)) * STAGE);   // [8][ROW]
+      const long slot = 2 * run + (tile0 == 0);
+      __syncwarp();
+      if (!all && lane == (tile0 == 0)) {   // the lane that cleared it
+        const long t0 = r.u + su - x + KV8_OVER, w0 = t0 / r.quota;
+        p.piece[slot] = {(int)((t0 + sh.tiles - 1) / r.quota - w0) + 1, (int)w0, sh.s0, q0, nq, h, {0, 0}};
+      }
+      float* so = reinterpret_cast<float*>(ring + (warp * 2 + 1) * HALF);   // [8][ROW]
+      static_assert(8 * ROW * 4 <= HALF, "");
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         __syncwarp();
@@ -929,76 +957,71 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_kernel(Kv8AttnP p) {
   }
 }
 
-// Merges the jobs that runs cut.  Every warp looks at the one or two cut jobs
-// that its run has a piece of, and takes its share of each one's columns (four channels
-// of a query) over all pieces: lanes over columns, and over pieces where the
-// share has fewer columns than lanes.
+// Merges the jobs that runs cut.  Block w looks at the one or two pieces that run
+// w left, and takes its share of each one's job's columns (four channels of a
+// query) over all pieces: threads over columns, and over pieces where the share
+// has fewer columns than threads.  Latency bounds it: a look at what the run left,
+// then loads that do not depend on one another.
+struct Kv8Sum {
+  float M, l;
+  float4 y;
+};
+__device__ __forceinline__ void kv8_join(Kv8Sum& a, float M, float l, float4 y) {
+  const float Mn = fmaxf(a.M, M), mu = Mn == -INFINITY ? 0.f : Mn, f = kv8_ex2(a.M - mu), g = kv8_ex2(M - mu);
+  a.M = Mn;
+  a.l = a.l * f + l * g;
+  a.y.x = a.y.x * f + y.x * g; a.y.y = a.y.y * f + y.y * g;
+  a.y.z = a.y.z * f + y.z * g; a.y.w = a.y.w * f + y.w * g;
+}
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_merge_kernel(Kv8AttnP p) {
-  constexpr int NQ = 8 * NT, C4 = D / 4, TILE = Kv8Tile<D>::TILE;
-  // lengths and starts were written before the attention kernel began, which this launch follows
-  Kv8Run r;
-  const bool any = kv8_locate<NQ, TILE, false>(p, r);
+  constexpr int NQ = 8 * NT, C4 = D / 4, NTH = 32 * KV8_NW;
+  __shared__ Kv8Sum part[KV8_NW][32];
   griddep_wait();
   griddep_release();
-  if (!any || r.u >= r.total || r.b < 0) return;
-  const int lane = threadIdx.x & 31;
-  const long run = (long)blockIdx.x * KV8_NW + (threadIdx.x >> 5), end = min(r.u + r.quota, r.total);
-  Kv8Share sh = kv8_share<NQ, TILE>(p, r.b);
-  long j0 = r.u - r.x;   // first unit of the job
-  int b = r.b, job = r.job;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, run = blockIdx.x;
+  const Kv8Piece left[2] = {p.piece[2 * run], p.piece[2 * run + 1]};
+#pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (k == 1) {
-      // the job that the run ends in
-      while (j0 + sh.tiles + KV8_OVER < end) {
-        const int w = sh.tiles + KV8_OVER;
-        const long ahead = min((end - 1 - j0) / w, (long)(sh.jobs - 1 - job));
-        if (ahead > 0) {
-          j0 += ahead * w;
-          job += (int)ahead;
-          continue;
-        }
-        j0 += w;
-        job = 0;
-        do {
-          if (++b >= p.q.B) return;
-          sh = kv8_share<NQ, TILE>(p, b);
-        } while (sh.jobs == 0);
-      }
-      if (j0 <= r.u) return;   // the first one, which is done
-    }
-    const long t0 = j0 + KV8_OVER, t1 = t0 + sh.tiles;   // its tiles
-    if (end <= t0) return;                               // no tile of it in this run, none of a later job
-    const long w0 = t0 / r.quota, w1 = (t1 - 1) / r.quota;
-    const int pieces = (int)(w1 - w0) + 1;
-    if (pieces == 1) continue;
-    const int h = job % p.L.Hkv, q0 = job / p.L.Hkv * NQ, nq = min(NQ, sh.n * p.G - q0), cols = nq * C4;
+    const int pieces = left[k].pieces, cols = left[k].nq * C4;
+    const long w0 = left[k].w0;
+    if (pieces == 0) continue;
     const int share = (cols + pieces - 1) / pieces, c0 = (int)(run - w0) * share, c1 = min(cols, c0 + share);
-    auto slot = [&](int s) -> long { return 2 * (w0 + s) + (s == 0); };
     int wide = 1;
-    while (wide < 32 && wide < c1 - c0) wide <<= 1;
+    while (wide < NTH && wide < c1 - c0) wide <<= 1;
     for (int cb = c0; cb < c1; cb += wide) {
-      const int col = cb + (lane & (wide - 1)), n = min(col, c1 - 1) / C4, d = (min(col, c1 - 1) % C4) * 4;
-      const int lanes = 32 / wide;
-      float M = -INFINITY, lt = 0.f;
-      for (int s = lane / wide; s < pieces; s += lanes) M = fmaxf(M, p.part_ml[(slot(s) * NQ + n) * 2]);
-      for (int o = wide; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float mu = M == -INFINITY ? 0.f : M;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int col = min(cb + (tid & (wide - 1)), c1 - 1), n = col / C4, d = (col % C4) * 4;
+      Kv8Sum a = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 4
-      for (int s = lane / wide; s < pieces; s += lanes) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot(s) * NQ + n) * 2);
-        const float4 v = *reinterpret_cast<const float4*>(p.part + (slot(s) * NQ + n) * D + d);
-        const float f = kv8_ex2(ml.x - mu);
-        lt += ml.y * f;
-        y.x += v.x * f; y.y += v.y * f; y.z += v.z * f; y.w += v.w * f;
+      for (int s = tid / wide; s < pieces; s += NTH / wide) {
+        const long at = (2 * (w0 + s) + (s == 0)) * NQ + n;
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+        kv8_join(a, ml.x, ml.y, *reinterpret_cast<const float4*>(p.part + at * D + d));
       }
       for (int o = wide; o < 32; o <<= 1) {
-        lt += __shfl_xor_sync(0xffffffffu, lt, o);
-        y.x += __shfl_xor_sync(0xffffffffu, y.x, o); y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
-        y.z += __shfl_xor_sync(0xffffffffu, y.z, o); y.w += __shfl_xor_sync(0xffffffffu, y.w, o);
+        const float M = __shfl_xor_sync(0xffffffffu, a.M, o), l = __shfl_xor_sync(0xffffffffu, a.l, o);
+        float4 y;
+        y.x = __shfl_xor_sync(0xffffffffu, a.y.x, o); y.y = __shfl_xor_sync(0xffffffffu, a.y.y, o);
+        y.z = __shfl_xor_sync(0xffffffffu, a.y.z, o); y.w = __shfl_xor_sync(0xffffffffu, a.y.w, o);
+        kv8_join(a, M, l, y);
       }
-      if (lane < wide && col < c1) kv8_out<T>(p, sh.s0, h, q0 + n, d, D, y, M, lt);
+      if (wide <= 32) {
+        // the warps hold different pieces of the same columns
+        __syncthreads();
+        part[warp][lane] = a;
+        __syncthreads();
+        if (tid >= wide) continue;
+        for (int w = 1; w < KV8_NW; ++w) kv8_join(a, part[w][lane].M, part[w][lane].l, part[w][lane].y);
+      } else if (wide == 64) {
+        // warps 2, 3 hold other pieces of the columns of 0, 1
+        __syncthreads();
+        if (warp >= 2) part[warp][lane] = a;
+        __syncthreads();
+        if (warp >= 2) continue;
+        kv8_join(a, part[warp + 2][lane].M, part[warp + 2][lane].l, part[warp + 2][lane].y);
+      }
+      if (cb + (tid & (wide - 1)) < c1) kv8_out<T>(p, left[k].s0, left[k].h, left[k].q0 + n, d, D, a.y, a.M, a.l);
     }
   }
 }
@@ -1011,6 +1034,8 @@ const char* kv8_check_cache(const gpt_kv8_cache* c) {
   if (c->kind != GPT_KV8_INT8 && c->kind != GPT_KV8_E4M3) return "unknown cache kind";
   if (c->n_layers < 1 || c->n_pages < 1 || c->n_kv_heads < 1 || c->n_kv_heads > 1024)
     return "n_layers, n_pages and n_kv_heads must be >= 1 (n_kv_heads <= 1024)";
+  if ((long)c->n_pages * c->n_kv_heads * (c->page * c->head_dim / 16) >= 0xffffffffL)
+    return "one layer's keys must be below 64 GB";
   if (c->head_dim != 16 && c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128)
     return "head_dim must be 16, 32, 64 or 128";
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return "page must be 16, 32, 64 or 128";
@@ -1070,13 +1095,12 @@ static cudaError_t append_t(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 gr
 
 struct Kv8Plan {
   int nt, blocks, whole;
-  size_t part, ml;   // floats
+  size_t part, ml, piece;   // floats (piece: in floats too)
 };
 // Queries a job: 8, 16 or 32 (16 at most for 128 channels, whose sums fill the
 // registers), by the mean number of queries a sequence; more of them read the
 // cache fewer times, fewer waste less of the products.  Blocks: as many as are
-// resident at once (three an SM by shared memory; two where the sums take 255
-// registers), or one per job where no job has more than KV8_WHOLE tiles.
+// resident at once, or one per job where no job has more than KV8_WHOLE tiles.
 static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
   static int sms = 0;
   if (!sms) {
@@ -1095,10 +1119,11 @@ static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
   const long jobs = (b.start ? (long)b.rows * G / nq + b.B : (long)b.B * ((G + nq - 1) / nq)) * c.n_kv_heads;
   const long tiles = ((long)b.max_pages * c.page + tile - 1) / tile;
   P.whole = tiles <= KV8_WHOLE;
-  const long resident = (P.nt == 4 || (P.nt == 2 && c.head_dim == 128) ? 2L : 3L) * (sms ? sms : 148);
+  const long resident = (long)kv8_resident(c.head_dim, P.nt) * (sms ? sms : 148);
   P.blocks = (int)(P.whole ? jobs : std::min(resident, (jobs * tiles + KV8_NW - 1) / KV8_NW));
   P.part = P.whole ? 0 : (size_t)P.blocks * KV8_NW * 2 * nq * c.head_dim;
   P.ml = P.whole ? 0 : (size_t)P.blocks * KV8_NW * 2 * nq * 2;
+  P.piece = P.whole ? 0 : (size_t)P.blocks * KV8_NW * 2 * (sizeof(Kv8Piece) / sizeof(float));
   return P;
 }
 
@@ -1126,7 +1151,7 @@ static cudaError_t attn_nt(const Kv8AttnP& p, const Kv8Plan& P, cudaStream_t s) 
   const cudaError_t e = attn_launch<T, D, NT, KIND, false>(p, P, s);
   if (e != cudaSuccess) return e;
   ++g_kernel_launches;
-  return launch_k(kv8_attn_merge_kernel<T, D, NT>, dim3(P.blocks), dim3(32 * KV8_NW), 0, s, p);
+  return launch_k(kv8_attn_merge_kernel<T, D, NT>, dim3(P.blocks * KV8_NW), dim3(32 * KV8_NW), 0, s, p);
 }
 template <typename T, int D, int KIND>
 static cudaError_t attn_d(const Kv8AttnP& p, const Kv8Plan& P, cudaStream_t s) {
@@ -1198,7 +1223,7 @@ int gpt_kv8_attention_work(const gpt_kv8_cache* c, const gpt_kv8_batch* b, int n
   if (!*why && !bytes) why = "bytes is NULL";
   if (*why) return kv8_refuse("gpt_kv8_attention_work", why);
   const Kv8Plan P = kv8_plan(*c, *b, n_heads);
-  *bytes = (P.part + P.ml) * sizeof(float);
+  *bytes = (P.part + P.ml + P.piece) * sizeof(float);
   return GPT_OK;
 }
 
@@ -1213,10 +1238,11 @@ int gpt_kv8_attention(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b,
   if (*why) return kv8_refuse("gpt_kv8_attention", why);
   if (b->B == 0 || b->rows == 0) return GPT_OK;
   const Kv8Plan P = kv8_plan(*c, *b, n_heads);
-  if (!P.whole && (!work || work_bytes < (P.part + P.ml) * sizeof(float) || ((uintptr_t)work & 15)))
+  if (!P.whole && (!work || work_bytes < (P.part + P.ml + P.piece) * sizeof(float) || ((uintptr_t)work & 15)))
     return kv8_refuse("gpt_kv8_attention", "work must be 16-byte aligned and hold gpt_kv8_attention_work bytes");
   Kv8AttnP p = {kv8_layer(*c, layer), kv8_seqs(*b), (const uint16_t*)q, (uint16_t*)out, lse, ldq, ldo,
-                n_heads, n_heads / c->n_kv_heads, b->max_pages * c->page, scale, (float*)work, (float*)work + P.part, err};
+                n_heads, n_heads / c->n_kv_heads, b->max_pages * c->page, scale, (float*)work, (float*)work + P.part,
+                (Kv8Piece*)((float*)work + P.part + P.ml), err};
   cudaStream_t s = (cudaStream_t)stream;
   const bool i8 = c->kind == GPT_KV8_INT8;
   const int D = c->head_dim;
