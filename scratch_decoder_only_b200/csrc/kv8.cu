@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(128) kv8_read_kernel(Kv8ReadP p) {
 // that jobs are short (KV8_WHOLE tiles at most), a block takes a whole job, its
 // four warps the tiles in turn, and merges it in shared memory: one kernel.
 // ---------------------------------------------------------------------------
-#define KV8_NW 4
+#define KV8_NW 4       // warps a block; KV8_WIDE where blocks take whole jobs and are few
+#define KV8_WIDE 8
 #define KV8_WHOLE 8
 #define KV8_OVER 2
 
@@ -383,68 +384,66 @@ __device__ __forceinline__ Kv8Share kv8_share(const Kv8AttnP& p, int b) {
 // [run * quota, (run + 1) * quota) of total.  All threads of the block call
 // this; false: no such run.
 struct Kv8Run {
-  int b, job, x;
-  long u, quota, total;
+  int b, job, x, u, quota, total;
 };
 template <int NQ, int TILE, bool WHOLE>
-__device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, long runs, long run0, Kv8Run& r) {
-  __shared__ long wsum[KV8_NW], sh_rem[KV8_NW];
-  __shared__ int sh_b[KV8_NW];
+__device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, int runs, int run0, Kv8Run& r) {
+  __shared__ int wsum[KV8_WIDE], sh_rem[KV8_NW], sh_b[KV8_NW];
   constexpr int PER = WHOLE ? 1 : KV8_NW;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.q.B;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.q.B, nth = blockDim.x, nw = nth >> 5;
   if (WHOLE && !p.q.start) {
     // the same jobs for each sequence
     const int per = (p.G + NQ - 1) / NQ * p.L.Hkv;
-    r.b = (int)(run0 / per);
-    r.job = (int)(run0 % per);
+    r.b = run0 / per;
+    r.job = run0 % per;
     r.x = KV8_OVER;
     return r.b < B;
   }
-  auto units = [&](int b) -> long {
+  auto units = [&](int b) -> int {
     if (b >= B) return 0;
     const Kv8Share s = kv8_share<NQ, TILE>(p, b);
-    return WHOLE ? s.jobs : (long)s.jobs * (s.tiles + KV8_OVER);
+    return WHOLE ? s.jobs : s.jobs * (s.tiles + KV8_OVER);
   };
-  const long mine = units(tid);   // of the first 128 sequences
+  const int mine = units(tid);   // of the first sequences
   r.total = 0;
   r.quota = 1;
-  long u0 = run0;
+  int u0 = run0;
   if (!WHOLE) {
-    long sum = mine;
-    for (int b = tid + 32 * KV8_NW; b < B; b += 32 * KV8_NW) sum += units(b);
-#pragma unroll
-    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    int sum = mine;
+    for (int b = tid + nth; b < B; b += nth) sum += units(b);
+    sum = __reduce_add_sync(0xffffffffu, sum);
     if (lane == 0) wsum[warp] = sum;
     __syncthreads();
-    for (int w = 0; w < KV8_NW; ++w) r.total += wsum[w];
-    r.quota = max((long)KV8_OVER + 1, (r.total + runs - 1) / runs);
+    for (int w = 0; w < nw; ++w) r.total += wsum[w];
+    r.quota = max(KV8_OVER + 1, (r.total - 1) / runs + 1);
+    if (run0 >= (r.total - 1) / r.quota + 1) return false;
     u0 = run0 * r.quota;
-    if (u0 >= r.total) return false;
     if (tid < PER) sh_b[tid] = -1;
   }
   const int ask = PER == 1 ? 0 : warp;
-  r.u = u0 + ask * r.quota;
-  const long u3 = WHOLE ? u0 : min(u0 + (PER - 1) * r.quota, r.total - 1);
-  long carry = 0;
-  for (int b0 = 0; b0 < B; b0 += 32 * KV8_NW) {
-    const long v = b0 ? units(b0 + tid) : mine;
-    long inc = v;
+  const int left = r.total - 1 - u0;   // units behind u0, not to pass 2^31
+  r.u = PER == 1 ? u0 : ask * r.quota <= left ? u0 + ask * r.quota : r.total;
+  const int u3 = WHOLE ? u0 : u0 + min((PER - 1) * r.quota, left);
+  int carry = 0;
+  for (int b0 = 0; b0 < B; b0 += nth) {
+    const int v = b0 ? units(b0 + tid) : mine;
+    int inc = v;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
-      const long y = __shfl_up_sync(0xffffffffu, inc, k);
+      const int y = __shfl_up_sync(0xffffffffu, inc, k);
       if (lane >= k) inc += y;
     }
     __syncthreads();
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    long first = carry + inc - v;
-    for (int w = 0; w < KV8_NW; ++w) {
+    int first = carry + inc - v;
+    for (int w = 0; w < nw; ++w) {
       if (w < warp) first += wsum[w];
       carry += wsum[w];
     }
     for (int w = 0; w < PER; ++w) {
-      const long u = u0 + w * r.quota;
-      if (u >= first && u < first + v) {
+      const int u = u0 + w * r.quota;
+      if (w * r.quota <= u3 - u0 && u >= first && u - first < v) {
         sh_b[w] = b0 + tid;
         sh_rem[w] = u - first;
       }
@@ -454,14 +453,14 @@ __device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, long runs, long ru
   if (WHOLE && carry <= u0) return false;
   __syncthreads();
   r.b = sh_b[ask];
-  const long rem = sh_rem[ask];
+  const int rem = sh_rem[ask];
   if (WHOLE) {
-    r.job = (int)rem;
+    r.job = rem;
     r.x = KV8_OVER;
   } else if (r.b >= 0) {
     const int w = kv8_share<NQ, TILE>(p, r.b).tiles + KV8_OVER;
-    r.job = (int)(rem / w);
-    r.x = (int)(rem % w);
+    r.job = rem / w;
+    r.x = rem % w;
   }
   return true;
 }
@@ -471,12 +470,13 @@ struct Kv8Tile {
   static constexpr int TILE = D == 128 ? 32 : 64;
   static constexpr int HALF = TILE * D;   // bytes of a tile's keys, and of its values
 };
-template <int D, int NT, bool WHOLE>
+// NW: warps a block that takes whole jobs (0: blocks of KV8_NW warps take runs)
+template <int D, int NT, int NW>
 constexpr size_t kv8_attn_smem() {
-  return (size_t)KV8_NW * 2 * Kv8Tile<D>::HALF + (WHOLE ? (size_t)2 * 8 * NT * (D + 4) * 4 : 0);
+  return (size_t)(NW ? NW : KV8_NW) * 2 * Kv8Tile<D>::HALF + (size_t)(NW / 2) * 8 * NT * (D + 4) * 4;
 }
-// Blocks an SM holds: what their registers allow (128, 168 and 255 a thread).
-__host__ __device__ constexpr int kv8_resident(int D, int nt) { return nt == 1 ? 4 : nt == 2 && D < 128 ? 3 : 2; }
+// Blocks of KV8_NW warps an SM holds: what their registers allow (128, 168 and 255 a thread).
+__host__ __device__ constexpr int kv8_resident(int D, int nt) { return nt == 1 ? 4 : D < 128 ? 3 : 2; }
 
 // The result of query q0 + n of a job, four channels from d on.
 template <typename T>
@@ -491,12 +491,15 @@ __device__ __forceinline__ void kv8_out(const Kv8AttnP& p, int s0, int h, int qi
   if (d == 0 && p.lse) p.lse[(long)row * p.H + hq] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * 0.6931471805599453f;
 }
 
-template <typename T, int D, int NT, int KIND, bool WHOLE>
-__global__ void __launch_bounds__(32 * KV8_NW, kv8_resident(D, NT)) kv8_attn_kernel(Kv8AttnP p) {
+template <typename T, int D, int NT, int KIND, int NW>
+__global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT) * KV8_NW / (NW ? NW : KV8_NW))
+    kv8_attn_kernel(Kv8AttnP p) {
+  constexpr bool WHOLE = NW != 0;
+  constexpr int WARPS = WHOLE ? NW : KV8_NW;
   constexpr int NQ = 8 * NT, KW = D / 16, TILE = Kv8Tile<D>::TILE, HALF = Kv8Tile<D>::HALF;
   constexpr int TQ = TILE / 4;                         // tokens of a quarter
   constexpr int KP = D / 4 < 16 ? D / 4 : 16, KT = D / 4 / KP;   // bytes of a key read, reads of a quarter key
-  constexpr int STEP = WHOLE ? KV8_NW : 1;
+  constexpr int STEP = WHOLE ? WARPS : 1;
   griddep_wait();
   griddep_release();
   extern __shared__ __align__(128) uint8_t ring[];
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(32 * KV8_NW, kv8_resident(D, NT)) kv8_attn_ker
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane >> 2, t = lane & 3;
   const int G = p.G, lp = L.lp, pmask = (1 << lp) - 1, Hkv = L.Hkv;
   if (blockIdx.x == 0) {
-    for (int b = threadIdx.x; b < p.q.B; b += 32 * KV8_NW) {
+    for (int b = threadIdx.x; b < p.q.B; b += 32 * WARPS) {
       if (p.q.start && (p.q.start[b] < 0 || p.q.start[b + 1] < p.q.start[b] || p.q.start[b + 1] > p.q.rows))
         set_dev_err(p.err, GPT_DEVERR_START);
       const Kv8Share s = kv8_share<NQ, TILE>(p, b);
@@ -512,13 +515,13 @@ __global__ void __launch_bounds__(32 * KV8_NW, kv8_resident(D, NT)) kv8_attn_ker
     }
   }
   Kv8Run r;
-  const long run = (long)blockIdx.x * KV8_NW + warp;
+  const int run = blockIdx.x * WARPS + warp;
   if (!WHOLE && lane < 2) p.piece[2 * run + lane].pieces = 0;
-  if (!kv8_locate<NQ, TILE, WHOLE>(p, (long)gridDim.x * KV8_NW, (long)blockIdx.x * (WHOLE ? 1 : KV8_NW), r)) return;
+  if (!kv8_locate<NQ, TILE, WHOLE>(p, gridDim.x * KV8_NW, blockIdx.x * (WHOLE ? 1 : KV8_NW), r)) return;
   if (!WHOLE && (r.u >= r.total || r.b < 0)) return;   // no barrier follows
   Kv8Share sh = kv8_share<NQ, TILE>(p, r.b);
   // units of this run, counted from its begin; a job's first KV8_OVER have no tile
-  const int R = WHOLE ? sh.tiles : (int)min(r.quota, r.total - r.u);
+  const int R = WHOLE ? sh.tiles : min(r.quota, r.total - r.u);
 
   // ---- the warp's next tile: sequence nb, head nh, tile nt of nm, the job's number nj of njobs; nu: the unit; the
   // page-and-head number of this lane's quarter (none: KV8_NONE)
@@ -848,10 +851,10 @@ __global__ void __launch_bounds__(32 * KV8_NW, kv8_resident(D, NT)) kv8_attn_ker
         }
       }
     if constexpr (WHOLE) {
-      // ---- merge the warps: 2, 3 into 0, 1, then 1 into 0, whose result goes out
+      // ---- merge the warps, the upper half into the lower one each time; warp 0's result goes out
       constexpr int ROW = D + 4;
-      float* so = reinterpret_cast<float*>(ring + KV8_NW * 2 * HALF);   // [2][NQ][ROW]
-      __shared__ float sm[2][NQ], sl[2][NQ];
+      float* so = reinterpret_cast<float*>(ring + WARPS * 2 * HALF);   // [WARPS / 2][NQ][ROW]
+      __shared__ float sm[WARPS / 2][NQ], sl[WARPS / 2][NQ];
       auto put = [&](int at) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -886,18 +889,17 @@ __global__ void __launch_bounds__(32 * KV8_NW, kv8_resident(D, NT)) kv8_attn_ker
             }
           }
       };
-      if (sh.tiles > 1) {   // else warp 0 has it all
-        if (warp >= 2) put(warp - 2);
+#pragma unroll
+      for (int half = WARPS / 2; half; half >>= 1) {
+        if (sh.tiles <= half) continue;   // those warps had no tile
+        if (warp >= half && warp < 2 * half) put(warp - half);
         __syncthreads();
-        if (warp < 2) take(warp);
+        if (warp < half) take(warp);
         __syncthreads();
-        if (warp == 1) put(1);
-        __syncthreads();
-        if (warp == 0) take(1);
       }
       if (warp == 0) put(0);
       __syncthreads();
-      for (int i = threadIdx.x; i < nq * (D / 4); i += 32 * KV8_NW) {
+      for (int i = threadIdx.x; i < nq * (D / 4); i += 32 * WARPS) {
         const int n = i / (D / 4), d = (i % (D / 4)) * 4;
         kv8_out<T>(p, sh.s0, h, q0 + n, d, D, *reinterpret_cast<const float4*>(so + n * ROW + d), sm[0][n], sl[0][n]);
       }
@@ -906,11 +908,11 @@ __global__ void __launch_bounds__(32 * KV8_NW, kv8_resident(D, NT)) kv8_attn_ker
       // ---- out, or to scratch, eight queries at a time through the values' buffer
       constexpr int ROW = D == 128 ? D : D + 4;
       const bool all = cnt == sh.tiles;
-      const long slot = 2 * run + (tile0 == 0);
+      const int slot = 2 * run + (tile0 == 0);
       __syncwarp();
       if (!all && lane == (tile0 == 0)) {   // the lane that cleared it
-        const long t0 = r.u + su - x + KV8_OVER, w0 = t0 / r.quota;
-        p.piece[slot] = {(int)((t0 + sh.tiles - 1) / r.quota - w0) + 1, (int)w0, sh.s0, q0, nq, h, {0, 0}};
+        const int t0 = r.u + su - x + KV8_OVER, w0 = t0 / r.quota;
+        p.piece[slot] = {(t0 + sh.tiles - 1) / r.quota - w0 + 1, w0, sh.s0, q0, nq, h, {0, 0}};
       }
       float* so = reinterpret_cast<float*>(ring + (warp * 2 + 1) * HALF);   // [8][ROW]
       static_assert(8 * ROW * 4 <= HALF, "");
@@ -935,7 +937,7 @@ __global__ void __launch_bounds__(32 * KV8_NW, kv8_resident(D, NT)) kv8_attn_ker
           if (all) {
             kv8_out<T>(p, sh.s0, h, q0 + j * 8 + n, d, D, y, M, lt);
           } else {
-            const long at = slot * NQ + j * 8 + n;
+            const long at = (long)slot * NQ + j * 8 + n;
             *reinterpret_cast<float4*>(p.part + at * D + d) = y;
             if (d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(M, lt);
           }
@@ -974,31 +976,53 @@ __device__ __forceinline__ void kv8_join(Kv8Sum& a, float M, float l, float4 y) 
   a.y.z = a.y.z * f + y.z * g; a.y.w = a.y.w * f + y.w * g;
 }
 
+// A column of job J over the pieces first, first + step, ...
+template <int NQ, int D>
+__device__ __forceinline__ Kv8Sum kv8_gather(const Kv8AttnP& p, const Kv8Piece& J, int col, int first, int step) {
+  constexpr int BATCH = 8;   // pieces whose loads are in flight together
+  const int n = col / (D / 4), d = (col % (D / 4)) * 4;
+  Kv8Sum a = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int s0 = first; s0 < J.pieces; s0 += BATCH * step) {
+    float2 ml[BATCH];
+    float4 y[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int s = min(s0 + i * step, J.pieces - 1);
+      const long at = (2 * (long)(J.w0 + s) + (s == 0)) * NQ + n;
+      ml[i] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+      y[i] = *reinterpret_cast<const float4*>(p.part + at * D + d);
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (s0 + i * step < J.pieces) kv8_join(a, ml[i].x, ml[i].y, y[i]);
+  }
+  return a;
+}
+#define KV8_MERGE 64   // threads
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_merge_kernel(Kv8AttnP p) {
-  constexpr int NQ = 8 * NT, C4 = D / 4, NTH = 32 * KV8_NW;
-  __shared__ Kv8Sum part[KV8_NW][32];
+__global__ void __launch_bounds__(KV8_MERGE) kv8_attn_merge_kernel(Kv8AttnP p) {
+  constexpr int NQ = 8 * NT, C4 = D / 4;
+  __shared__ Kv8Sum part[32];
   griddep_wait();
   griddep_release();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, run = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, run = blockIdx.x;
   const Kv8Piece left[2] = {p.piece[2 * run], p.piece[2 * run + 1]};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int pieces = left[k].pieces, cols = left[k].nq * C4;
-    const long w0 = left[k].w0;
-    if (pieces == 0) continue;
-    const int share = (cols + pieces - 1) / pieces, c0 = (int)(run - w0) * share, c1 = min(cols, c0 + share);
-    int wide = 1;
-    while (wide < NTH && wide < c1 - c0) wide <<= 1;
-    for (int cb = c0; cb < c1; cb += wide) {
-      const int col = min(cb + (tid & (wide - 1)), c1 - 1), n = col / C4, d = (col % C4) * 4;
-      Kv8Sum a = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
-      for (int s = tid / wide; s < pieces; s += NTH / wide) {
-        const long at = (2 * (w0 + s) + (s == 0)) * NQ + n;
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-        kv8_join(a, ml.x, ml.y, *reinterpret_cast<const float4*>(p.part + at * D + d));
-      }
+    const Kv8Piece& J = left[k];
+    if (J.pieces == 0) continue;
+    const int i = run - J.w0, cols = J.nq * C4;
+    const int c0 = (int)((long)i * cols / J.pieces), c1 = (int)((long)(i + 1) * cols / J.pieces);
+    auto out = [&](const Kv8Sum& a, int col) {
+      kv8_out<T>(p, J.s0, J.h, J.q0 + col / C4, (col % C4) * 4, D, a.y, a.M, a.l);
+    };
+    if (c1 - c0 > 32) {
+      for (int col = c0 + tid; col < c1; col += KV8_MERGE) out(kv8_gather<NQ, D>(p, J, col, 0, 1), col);
+    } else if (c0 < c1) {
+      int wide = 1;
+      while (wide < c1 - c0) wide <<= 1;
+      const int col = min(c0 + (lane & (wide - 1)), c1 - 1);
+      Kv8Sum a = kv8_gather<NQ, D>(p, J, col, tid / wide, KV8_MERGE / wide);
       for (int o = wide; o < 32; o <<= 1) {
         const float M = __shfl_xor_sync(0xffffffffu, a.M, o), l = __shfl_xor_sync(0xffffffffu, a.l, o);
         float4 y;
@@ -1006,22 +1030,13 @@ __global__ void __launch_bounds__(32 * KV8_NW) kv8_attn_merge_kernel(Kv8AttnP p)
         y.z = __shfl_xor_sync(0xffffffffu, a.y.z, o); y.w = __shfl_xor_sync(0xffffffffu, a.y.w, o);
         kv8_join(a, M, l, y);
       }
-      if (wide <= 32) {
-        // the warps hold different pieces of the same columns
+      if (J.pieces > 32 / wide) {   // the second warp has some
         __syncthreads();
-        part[warp][lane] = a;
+        if (tid >= 32) part[lane] = a;
         __syncthreads();
-        if (tid >= wide) continue;
-        for (int w = 1; w < KV8_NW; ++w) kv8_join(a, part[w][lane].M, part[w][lane].l, part[w][lane].y);
-      } else if (wide == 64) {
-        // warps 2, 3 hold other pieces of the columns of 0, 1
-        __syncthreads();
-        if (warp >= 2) part[warp][lane] = a;
-        __syncthreads();
-        if (warp >= 2) continue;
-        kv8_join(a, part[warp + 2][lane].M, part[warp + 2][lane].l, part[warp + 2][lane].y);
+        if (tid < 32) kv8_join(a, part[lane].M, part[lane].l, part[lane].y);
       }
-      if (cb + (tid & (wide - 1)) < c1) kv8_out<T>(p, left[k].s0, left[k].h, left[k].q0 + n, d, D, a.y, a.M, a.l);
+      if (tid < wide && c0 + tid < c1) out(a, c0 + tid);
     }
   }
 }
@@ -1094,13 +1109,20 @@ static cudaError_t append_t(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 gr
 }
 
 struct Kv8Plan {
-  int nt, blocks, whole;
-  size_t part, ml, piece;   // floats (piece: in floats too)
+  int nt, blocks, warps;   // warps of blocks that take whole jobs, or 0
+  bool fits;
+  size_t part, ml, piece;  // floats (piece: in floats too)
 };
-// Queries a job: 8, 16 or 32 (16 at most for 128 channels, whose sums fill the
-// registers), by the mean number of queries a sequence; more of them read the
-// cache fewer times, fewer waste less of the products.  Blocks: as many as are
-// resident at once, or one per job where no job has more than KV8_WHOLE tiles.
+// Queries a job: 16 where that saves enough passes over the cache.  A pass with
+// 16 queries costs 1.7 of one with 8 (64 x 4096 tokens in L2: 12 warps an SM
+// instead of 16, and 1.3 times the instructions), so they are taken for 9 to 16
+// queries a sequence (70 against 90 us for 16 of 64 channels) and 25 to 32; where the
+// sequences' rows differ, only their mean is known here, and half a job is lost
+// a sequence on average: from 19 on (mean 12, one to five rows of four heads: 48
+// us with 8, 61 with 16).  Jobs of 32 queries were no faster than two of 16.
+//
+// Blocks: as many as are resident at once, or one per job where no job has more
+// than KV8_WHOLE tiles; those have twice the warps where they leave SMs idle.
 static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
   static int sms = 0;
   if (!sms) {
@@ -1111,55 +1133,57 @@ static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
     else
       cudaGetLastError();
   }
-  Kv8Plan P;
-  const int G = H / c.n_kv_heads, tile = c.head_dim == 128 ? 32 : 64;
-  const long per = b.B ? ((long)b.rows + b.B - 1) / b.B * G : G;
-  P.nt = per <= 8 ? 1 : per <= 16 || c.head_dim == 128 ? 2 : 4;
+  Kv8Plan P = {};
+  const int G = H / c.n_kv_heads, tile = c.head_dim == 128 ? 32 : 64, nsm = sms ? sms : 148;
+  const long mean = b.B ? ((long)b.rows * G + b.B - 1) / b.B : G;
+  P.nt = (b.start && b.rows != b.B ? mean > 18 : 10 * ((G + 7) / 8) > 17 * ((G + 15) / 16)) ? 2 : 1;
   const int nq = 8 * P.nt;
   const long jobs = (b.start ? (long)b.rows * G / nq + b.B : (long)b.B * ((G + nq - 1) / nq)) * c.n_kv_heads;
   const long tiles = ((long)b.max_pages * c.page + tile - 1) / tile;
-  P.whole = tiles <= KV8_WHOLE;
-  const long resident = (long)kv8_resident(c.head_dim, P.nt) * (sms ? sms : 148);
-  P.blocks = (int)(P.whole ? jobs : std::min(resident, (jobs * tiles + KV8_NW - 1) / KV8_NW));
-  P.part = P.whole ? 0 : (size_t)P.blocks * KV8_NW * 2 * nq * c.head_dim;
-  P.ml = P.whole ? 0 : (size_t)P.blocks * KV8_NW * 2 * nq * 2;
-  P.piece = P.whole ? 0 : (size_t)P.blocks * KV8_NW * 2 * (sizeof(Kv8Piece) / sizeof(float));
+  P.fits = jobs * (tiles + KV8_OVER) <= 0x7fffffffL;   // units are counted in 32 bits
+  if (tiles <= KV8_WHOLE) {
+    P.blocks = (int)jobs;
+    P.warps = jobs * 2 <= nsm * kv8_resident(c.head_dim, P.nt) ? KV8_WIDE : KV8_NW;
+    return P;
+  }
+  P.blocks = (int)std::min((long)kv8_resident(c.head_dim, P.nt) * nsm, (jobs * tiles + KV8_NW - 1) / KV8_NW);
+  const size_t slots = (size_t)P.blocks * KV8_NW * 2;
+  P.part = slots * nq * c.head_dim;
+  P.ml = slots * nq * 2;
+  P.piece = slots * (sizeof(Kv8Piece) / sizeof(float));
   return P;
 }
 
-template <typename T, int D, int NT, int KIND, bool WHOLE>
+template <typename T, int D, int NT, int KIND, int NW>
 static cudaError_t attn_launch(const Kv8AttnP& p, const Kv8Plan& P, cudaStream_t s) {
-  constexpr size_t smem = kv8_attn_smem<D, NT, WHOLE>();
-  if (smem > 48000) {
+  constexpr size_t smem = kv8_attn_smem<D, NT, NW>();
+  if (smem > 40000) {
     static bool ready[64] = {};   // per device: the attribute is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !ready[dev]) {
-      e = cudaFuncSetAttribute(kv8_attn_kernel<T, D, NT, KIND, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(kv8_attn_kernel<T, D, NT, KIND, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)smem);
       if (e != cudaSuccess) return e;
       if (dev < 64) ready[dev] = true;
     }
   }
   ++g_kernel_launches;
-  return launch_k(kv8_attn_kernel<T, D, NT, KIND, WHOLE>, dim3(P.blocks), dim3(32 * KV8_NW), smem, s, p);
+  return launch_k(kv8_attn_kernel<T, D, NT, KIND, NW>, dim3(P.blocks), dim3(32 * (NW ? NW : KV8_NW)), smem, s, p);
 }
 template <typename T, int D, int NT, int KIND>
 static cudaError_t attn_nt(const Kv8AttnP& p, const Kv8Plan& P, cudaStream_t s) {
-  if (P.whole) return attn_launch<T, D, NT, KIND, true>(p, P, s);
-  const cudaError_t e = attn_launch<T, D, NT, KIND, false>(p, P, s);
+  if (P.warps == KV8_WIDE) return attn_launch<T, D, NT, KIND, KV8_WIDE>(p, P, s);
+  if (P.warps == KV8_NW) return attn_launch<T, D, NT, KIND, KV8_NW>(p, P, s);
+  const cudaError_t e = attn_launch<T, D, NT, KIND, 0>(p, P, s);
   if (e != cudaSuccess) return e;
   ++g_kernel_launches;
-  return launch_k(kv8_attn_merge_kernel<T, D, NT>, dim3(P.blocks * KV8_NW), dim3(32 * KV8_NW), 0, s, p);
+  return launch_k(kv8_attn_merge_kernel<T, D, NT>, dim3(P.blocks * KV8_NW), dim3(KV8_MERGE), 0, s, p);
 }
 template <typename T, int D, int KIND>
 static cudaError_t attn_d(const Kv8AttnP& p, const Kv8Plan& P, cudaStream_t s) {
-  if (P.nt == 1) return attn_nt<T, D, 1, KIND>(p, P, s);
-  if constexpr (D < 128) {
-    if (P.nt == 4) return attn_nt<T, D, 4, KIND>(p, P, s);
-  }
-  return attn_nt<T, D, 2, KIND>(p, P, s);
+  return P.nt == 1 ? attn_nt<T, D, 1, KIND>(p, P, s) : attn_nt<T, D, 2, KIND>(p, P, s);
 }
 template <typename T, int KIND>
 static cudaError_t attn_t(const Kv8AttnP& p, const Kv8Plan& P, int D, cudaStream_t s) {
@@ -1238,7 +1262,8 @@ int gpt_kv8_attention(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b,
   if (*why) return kv8_refuse("gpt_kv8_attention", why);
   if (b->B == 0 || b->rows == 0) return GPT_OK;
   const Kv8Plan P = kv8_plan(*c, *b, n_heads);
-  if (!P.whole && (!work || work_bytes < (P.part + P.ml + P.piece) * sizeof(float) || ((uintptr_t)work & 15)))
+  if (!P.fits) return kv8_refuse("gpt_kv8_attention", "too many queries and tokens");
+  if (!P.warps && (!work || work_bytes < (P.part + P.ml + P.piece) * sizeof(float) || ((uintptr_t)work & 15)))
     return kv8_refuse("gpt_kv8_attention", "work must be 16-byte aligned and hold gpt_kv8_attention_work bytes");
   Kv8AttnP p = {kv8_layer(*c, layer), kv8_seqs(*b), (const uint16_t*)q, (uint16_t*)out, lse, ldq, ldo,
                 n_heads, n_heads / c->n_kv_heads, b->max_pages * c->page, scale, (float*)work, (float*)work + P.part,
