@@ -503,7 +503,7 @@ int gpt_kv8_attention_work(const gpt_kv8_cache* c, const gpt_kv8_batch* b, int n
  *         a row are its pages; the others are never read, and -1 once freed
  *  lens   device int32 [n_rows]: tokens of each row (0: empty)
  *  ref    device int32 [n_pages]: rows that hold the page (0: free)
- * All zero lens and refs is an empty pool.  n_rows <= 16384. */
+ * All zero lens and refs is an empty pool.  n_rows <= 16384, n_pages <= 2^24. */
 typedef struct {
   int32_t *table, *lens, *ref;
   int32_t n_rows, max_pages, ld_table, n_pages, page;

@@ -42,19 +42,22 @@ __device__ __forceinline__ int kv8_page(const Kv8Seqs& q, const Kv8Layer& L, int
 }
 
 // ---------------------------------------------------------------------------
-// Append.  One block of 128 threads per (page touched, head, keys | values).
-// The page's new rows stay in registers (VPT 16-byte vectors a thread) between
-// their largest magnitude (an unsigned 16-bit maximum over the bit patterns
-// without the sign, in which infinities and NaNs are the largest) and their
-// codes, so every input byte is read once.  Value codes are turned over through
-// shared memory: 16 tokens of a channel leave in one 16-byte store.  The work
-// is a copy with a maximum; bytes bound it, for single tokens the launch does.
+// Append.  A block of 128 threads takes a page of a sequence and a run of heads,
+// keys or values, one head after the other.  A head's new rows stay in registers
+// (VPT 16-byte vectors a thread) between their largest magnitude (an unsigned
+// 16-bit maximum over the bit patterns without the sign, in which infinities and
+// NaNs are the largest) and their codes, so every input byte is read once; the
+// next head's rows are loaded as soon as these are codes.  Value codes are turned over through shared
+// memory, four tokens by four channels at a time, and leave as 16 tokens of a
+// channel.  Bytes bound it for prompts, the launch for single tokens, whose
+// blocks take one head each.
 // ---------------------------------------------------------------------------
 struct Kv8AppendP {
   Kv8Layer L;
   Kv8Seqs q;
   const uint16_t *k, *v;
   long ldk, ldv;
+  int heads;   // a block's
   unsigned* err;
 };
 
@@ -66,6 +69,16 @@ __device__ __forceinline__ float bits16_f(unsigned b) {
   return to_f(*reinterpret_cast<const T*>(&u));
 }
 
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (std::is_same<T, f16>::value) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
 // one 16-byte vector of values times inv, as eight codes
 template <typename T, int KIND>
 __device__ __forceinline__ uint2 kv8_code8(const uint4& x, float inv) {
@@ -84,117 +97,143 @@ __device__ __forceinline__ uint32_t kv8_recode4(uint32_t w, float ratio) {
   return kv8_code4<KIND>(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
 }
 
+// Bytes 0 .. n - 1 of four.
+__device__ __forceinline__ uint32_t kv8_bytes(int n) { return n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u; }
+// w[i] = channels of token i  ->  w[i] = tokens of channel i
+__device__ __forceinline__ void kv8_turn4(uint32_t* w) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+  const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+  w[0] = __byte_perm(a, b, 0x5410);
+  w[1] = __byte_perm(a, b, 0x7632);
+  w[2] = __byte_perm(c, d, 0x5410);
+  w[3] = __byte_perm(c, d, 0x7632);
+}
+
+// (the second bound: 96 registers a thread up to 8 vectors, so that enough blocks are resident to cover a block's chain
+// of dependent loads)
 template <typename T, int KIND, int VPT>
-__global__ void __launch_bounds__(128) kv8_append_kernel(Kv8AppendP p) {
+__global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8AppendP p) {
   griddep_wait();
   griddep_release();
   extern __shared__ __align__(16) uint8_t turn[];   // value codes [P][D + KV8_PAD]
-  __shared__ unsigned wmax[4];
+  __shared__ unsigned wmax[2][4];
   const Kv8Layer& L = p.L;
-  const int tid = threadIdx.x, h = blockIdx.y, lp = L.lp, ld = L.ld, D = 1 << ld;
+  const int tid = threadIdx.x, lp = L.lp, ld = L.ld, D = 1 << ld;
+  const int h0 = blockIdx.y * p.heads, h1 = min(h0 + p.heads, L.Hkv);
   const bool is_v = blockIdx.z != 0;
   Kv8Unit u;
   if (!kv8_unit(p.q, blockIdx.x, lp, p.q.max_pages << lp, u, p.err)) return;
   const int id = kv8_page(p.q, L, u.b, u.unit, p.err);
   if (id < 0) return;
   const long ldx = is_v ? p.ldv : p.ldk;
-  const uint16_t* x = (is_v ? p.v : p.k) + (long)u.row * ldx + (h << ld);
+  const uint16_t* x = (is_v ? p.v : p.k) + (long)u.row * ldx;
+  float* scales = (is_v ? L.vs : L.ks) + (size_t)id * L.Hkv;
   const int nv = (u.hi - u.lo) << (ld - 3);
+  // vector tid + 128 j of a head: this thread's first one, and 128 vectors further
+  const int mine = (nv - tid + 127) >> 7;   // vectors of this thread
+  const long step = (128L >> (ld - 3)) * ldx;
+  x += (long)(tid >> (ld - 3)) * ldx + ((tid & ((D >> 3) - 1)) << 3);
   uint4 r[VPT];
-  unsigned mx = 0;
+  float s_old = 0.f;
+  auto load = [&](int h) {
+    const uint16_t* y = x + (h << ld);
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int i = tid + j * 128;
-    r[j] = i < nv ? *reinterpret_cast<const uint4*>(x + (long)(i >> (ld - 3)) * ldx + ((i & ((D >> 3) - 1)) << 3))
-                  : make_uint4(0, 0, 0, 0);
-  }
-  const size_t ph = (size_t)id * L.Hkv + h;
-  float* sp = (is_v ? L.vs : L.ks) + ph;
-  const float s_old = u.lo > 0 ? *sp : 0.f;   // read by all before the barrier, written behind it
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const unsigned a = __vmaxu2(__vmaxu2(r[j].x & 0x7fff7fffu, r[j].y & 0x7fff7fffu),
-                                __vmaxu2(r[j].z & 0x7fff7fffu, r[j].w & 0x7fff7fffu));
-    mx = max(mx, max(a & 0xffffu, a >> 16));
-  }
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  if ((tid & 31) == 0) wmax[tid >> 5] = mx;
-  __syncthreads();
-  mx = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
-  constexpr float TOP = KIND == GPT_KV8_INT8 ? 127.f : 448.f;
-  const float a = bits16_f<T>(mx);
-  float s = a / TOP;
-  if (s < FLT_MIN) s = 0.f;             // 1 / s would overflow
-  if (s_old > s) s = s_old;
-  if (!(a <= FLT_MAX) || s_old != s_old) s = NAN;
-  const bool live = s > 0.f;            // false for 0 and NaN: every code of the page is 0
-  const float inv = live ? 1.f / s : 0.f;
-  const bool recode = u.lo > 0 && s != s_old;
-  const float ratio = live ? s_old / s : 0.f;
-  if (tid == 0) *sp = s;
-  uint8_t* page = (is_v ? L.v : L.k) + (ph << (lp + ld));
-  if (!is_v) {
-    if (recode) {
-      uint32_t* o = reinterpret_cast<uint32_t*>(page);
-      for (int i = tid; i < (u.lo << (ld - 2)); i += 128) o[i] = live ? kv8_recode4<KIND>(o[i], ratio) : 0u;
-    }
-    uint2* o = reinterpret_cast<uint2*>(page + (u.lo << ld));
+    for (int j = 0; j < VPT; ++j, y += step) r[j] = j < mine ? *reinterpret_cast<const uint4*>(y) : make_uint4(0, 0, 0, 0);
+    s_old = u.lo > 0 ? scales[h] : 0.f;   // read by all before the barrier, written behind it
+  };
+  load(h0);
+  for (int h = h0; h < h1; ++h) {
+    unsigned mx = 0;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int i = tid + j * 128;
-      if (i < nv) o[i] = live ? kv8_code8<T, KIND>(r[j], inv) : make_uint2(0, 0);
+      const unsigned a = __vmaxu2(__vmaxu2(r[j].x & 0x7fff7fffu, r[j].y & 0x7fff7fffu),
+                                  __vmaxu2(r[j].z & 0x7fff7fffu, r[j].w & 0x7fff7fffu));
+      mx = max(mx, max(a & 0xffffu, a >> 16));
     }
-    return;
-  }
-  const int row = D + KV8_PAD;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int i = tid + j * 128;
-    if (i < nv)
-      *reinterpret_cast<uint2*>(turn + (u.lo + (i >> (ld - 3))) * row + ((i & ((D >> 3) - 1)) << 3)) =
-          live ? kv8_code8<T, KIND>(r[j], inv) : make_uint2(0, 0);
-  }
-  __syncthreads();
-  // 16-token groups that change: those with new tokens, all earlier ones too when the scale grew
-  const int g0 = recode ? 0 : u.lo >> 4, g1 = (u.hi + 15) >> 4;
-  uint4* o = reinterpret_cast<uint4*>(page);
-  for (int i = (g0 << ld) + tid; i < (g1 << ld); i += 128) {
-    const int t0 = (i >> ld) << 4, d = i & (D - 1);
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (t0 < u.lo) {
-      const uint4 old = o[i];
-      w[0] = old.x; w[1] = old.y; w[2] = old.z; w[3] = old.w;
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if ((tid & 31) == 0) wmax[h & 1][tid >> 5] = mx;
+    __syncthreads();   // (also: the turning buffer's codes of the head before have been read)
+    mx = max(max(wmax[h & 1][0], wmax[h & 1][1]), max(wmax[h & 1][2], wmax[h & 1][3]));
+    constexpr float TOP = KIND == GPT_KV8_INT8 ? 127.f : 448.f;
+    const float a = bits16_f<T>(mx);
+    float s = a / TOP;
+    if (s < FLT_MIN) s = 0.f;             // 1 / s would overflow
+    if (s_old > s) s = s_old;
+    if (!(a <= FLT_MAX) || s_old != s_old) s = NAN;
+    const bool live = s > 0.f;            // false for 0 and NaN: every code of the page is 0
+    const float inv = live ? 1.f / s : 0.f;
+    const bool recode = u.lo > 0 && s != s_old;
+    const float ratio = live ? s_old / s : 0.f;
+    if (tid == 0) scales[h] = s;
+    uint8_t* page = (is_v ? L.v : L.k) + (((size_t)id * L.Hkv + h) << (lp + ld));
+    const int row = D + KV8_PAD;
+    if (!is_v) {
       if (recode) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) w[q] = live ? kv8_recode4<KIND>(w[q], ratio) : 0u;
+        uint32_t* o = reinterpret_cast<uint32_t*>(page);
+        for (int i = tid; i < (u.lo << (ld - 2)); i += 128) o[i] = live ? kv8_recode4<KIND>(o[i], ratio) : 0u;
       }
-    }
+      uint2* o = reinterpret_cast<uint2*>(page + (u.lo << ld)) + tid;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t n = 0, keep = 0;
+      for (int j = 0; j < VPT; ++j)
+        if (j < mine) o[128 * j] = live ? kv8_code8<T, KIND>(r[j], inv) : make_uint2(0, 0);
+    } else {
+      uint8_t* o = turn + (u.lo + (tid >> (ld - 3))) * row + ((tid & ((D >> 3) - 1)) << 3);
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (j < mine)
+          *reinterpret_cast<uint2*>(o + j * (128 >> (ld - 3)) * row) =
+              live ? kv8_code8<T, KIND>(r[j], inv) : make_uint2(0, 0);
+    }
+    if (h + 1 < h1) load(h + 1);
+    if (!is_v) continue;
+    __syncthreads();
+    // 16-token groups that change: those with new tokens, all earlier ones too when the scale grew; a thread
+    // takes four channels of one
+    const int g0 = recode ? 0 : u.lo >> 4, g1 = (u.hi + 15) >> 4;
+    for (int i = (g0 << (ld - 2)) + tid; i < (g1 << (ld - 2)); i += 128) {
+      const int t0 = (i >> (ld - 2)) << 4, d = (i << 2) & (D - 1);
+      uint32_t w[4][4];   // [four tokens][channel]
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[q][e] = *reinterpret_cast<const uint32_t*>(turn + (t0 + 4 * q + e) * row + d);
+        kv8_turn4(w[q]);
+      }
+      uint4* o = reinterpret_cast<uint4*>(page + ((size_t)t0 << ld) + (d << 4));
+      if (t0 >= u.lo && t0 + 16 <= u.hi) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = make_uint4(w[0][e], w[1][e], w[2][e], w[3][e]);
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int t = t0 + 4 * q + e;
-        if (t < u.lo) keep |= 0xffu << (8 * e);
-        else if (t < u.hi) n |= (uint32_t)turn[t * row + d] << (8 * e);
+        const uint4 old = o[e];
+        const uint32_t was[4] = {old.x, old.y, old.z, old.w};
+        uint32_t z[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t keep = kv8_bytes(u.lo - t0 - 4 * q), upto = kv8_bytes(u.hi - t0 - 4 * q);
+          const uint32_t held = recode ? (live ? kv8_recode4<KIND>(was[q], ratio) : 0u) : was[q];
+          z[q] = (held & keep) | (w[q][e] & upto & ~keep);
+        }
+        o[e] = make_uint4(z[0], z[1], z[2], z[3]);
       }
-      w[q] = (w[q] & keep) | n;
     }
-    o[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Read back.  One block of 128 threads per (16 tokens, 128 channels of the
-// concatenated heads, keys | values), one 16-byte load of codes a thread:
-// 16 channels of a token (keys), or 16 tokens of a channel, turned over through
-// shared memory (values).
+// Read back.  A block of 128 threads takes 16 tokens, keys or values, and a run of
+// 128-channel columns of the concatenated heads, one 16-byte load of codes a
+// thread and column, the next two ahead: 16 channels of a token (keys), or 16
+// tokens of a channel, turned over through shared memory (values).
 // ---------------------------------------------------------------------------
 struct Kv8ReadP {
   Kv8Layer L;
   Kv8Seqs q;
   uint16_t *k, *v;
   long ldk, ldv;
+  int cols;   // a block's columns
   unsigned* err;
 };
 
@@ -202,9 +241,10 @@ template <typename T, int KIND>
 __global__ void __launch_bounds__(128) kv8_read_kernel(Kv8ReadP p) {
   griddep_wait();
   griddep_release();
-  __shared__ __align__(16) uint16_t tile[16][128 + 8];
+  __shared__ __align__(16) uint16_t tile[2][16][128 + 8];
   const Kv8Layer& L = p.L;
-  const int tid = threadIdx.x, lp = L.lp, ld = L.ld, D = 1 << ld, C = L.Hkv << ld, c0 = blockIdx.y * 128;
+  const int tid = threadIdx.x, lp = L.lp, ld = L.ld, D = 1 << ld, C = L.Hkv << ld;
+  const int b0 = blockIdx.y * p.cols * 128, b1 = min(b0 + p.cols * 128, C);
   const bool is_v = blockIdx.z != 0;
   Kv8Unit u;
   if (!kv8_unit(p.q, blockIdx.x, 4, p.q.max_pages << lp, u, p.err)) return;
@@ -212,44 +252,51 @@ __global__ void __launch_bounds__(128) kv8_read_kernel(Kv8ReadP p) {
   if (id < 0) return;
   const int slot0 = (u.unit << 4) & ((1 << lp) - 1);
   // this thread's 16 codes: channels c .. c + 15 of token t, or tokens 0 .. 15 of channel c
-  const int t = tid >> 3, c = c0 + (is_v ? tid : (tid & 7) << 4), h = c >> ld, d = c & (D - 1);
-  uint16_t y[16];
-  if (c < C) {
-    const size_t ph = (size_t)id * L.Hkv + h;
-    const uint8_t* page = (is_v ? L.v : L.k) + (ph << (lp + ld)) + ((size_t)slot0 << ld);
-    const uint4 w = *reinterpret_cast<const uint4*>(page + (is_v ? d << 4 : (t << ld) + d));
-    const float s = (is_v ? L.vs : L.ks)[ph];
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+  const int t = tid >> 3, cv = (tid & 7) << 4;
+  const uint8_t* codes = (is_v ? L.v : L.k) + (((size_t)id * L.Hkv) << (lp + ld)) + ((size_t)slot0 << ld);
+  const float* scales = (is_v ? L.vs : L.ks) + (size_t)id * L.Hkv;
+  uint4 next[2] = {};
+  float s_next[2] = {};
+  auto load = [&](int c0, int at) {
+    const int c = c0 + (is_v ? tid : cv), h = c >> ld, d = c & (D - 1);
+    if (c0 >= b1 || c >= C) return;
+    next[at] = *reinterpret_cast<const uint4*>(codes + ((size_t)h << (lp + ld)) + (is_v ? d << 4 : (t << ld) + d));
+    s_next[at] = scales[h];
+  };
+  uint16_t* out = (is_v ? p.v : p.k) + (long)(u.row + t - u.lo) * (is_v ? p.ldv : p.ldk) + cv;
+  const bool mine = t >= u.lo && t < u.hi;
+  load(b0, 0);
+  load(b0 + 128, 1);
+  for (int c0 = b0, par = 0; c0 < b1; c0 += 128, par ^= 1) {
+    const uint32_t w[4] = {next[0].x, next[0].y, next[0].z, next[0].w};
+    const float s = s_next[0];
+    next[0] = next[1];
+    s_next[0] = s_next[1];
+    load(c0 + 256, 1);
+    uint32_t y[8];   // pairs of 16-bit values
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t lo, hi;
-      kv8_widen<KIND>(ww[i], lo, hi);
+      kv8_widen<KIND>(w[i], lo, hi);
       const float2 a = f16x2_float(lo), b = f16x2_float(hi);
-      const float f[4] = {a.x * s, a.y * s, b.x * s, b.y * s};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const T r = from_f<T>(f[e]);
-        y[4 * i + e] = *reinterpret_cast<const uint16_t*>(&r);
-      }
+      y[2 * i] = pack16<T>(a.x * s, a.y * s);
+      y[2 * i + 1] = pack16<T>(b.x * s, b.y * s);
     }
-  }
-  const int cv = c0 + ((tid & 7) << 4);
-  if (is_v) {
+    if (is_v) {
+      // (two tiles in turn: one barrier keeps a tile's readers ahead of its next writers)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) tile[i][tid] = c < C ? y[i] : (uint16_t)0;
-    __syncthreads();
-  }
-  if (cv >= C || t < u.lo || t >= u.hi) return;
-  uint4* o = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + (long)(u.row + t - u.lo) * (is_v ? p.ldv : p.ldk) + cv);
-  if (is_v) {
-    o[0] = *reinterpret_cast<const uint4*>(&tile[t][(tid & 7) << 4]);
-    o[1] = *reinterpret_cast<const uint4*>(&tile[t][((tid & 7) << 4) + 8]);
-  } else {
-    uint32_t z[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = (uint32_t)y[2 * i] | (uint32_t)y[2 * i + 1] << 16;
-    o[0] = make_uint4(z[0], z[1], z[2], z[3]);
-    o[1] = make_uint4(z[4], z[5], z[6], z[7]);
+      for (int i = 0; i < 16; ++i) tile[par][i][tid] = (uint16_t)(y[i >> 1] >> (16 * (i & 1)));
+      __syncthreads();
+    }
+    if (!mine || c0 + cv >= C) continue;
+    uint4* o = reinterpret_cast<uint4*>(out + c0);
+    if (is_v) {
+      o[0] = *reinterpret_cast<const uint4*>(&tile[par][t][cv]);
+      o[1] = *reinterpret_cast<const uint4*>(&tile[par][t][cv + 8]);
+    } else {
+      o[0] = make_uint4(y[0], y[1], y[2], y[3]);
+      o[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
   }
 }
 
@@ -484,10 +531,8 @@ __device__ __forceinline__ void kv8_out(const Kv8AttnP& p, int s0, int h, int qi
                                         float lt) {
   const int row = s0 + qi / p.G, hq = h * p.G + qi % p.G;
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  union { T v[4]; uint2 u; } z;
-  z.v[0] = from_f<T>(y.x * inv); z.v[1] = from_f<T>(y.y * inv);
-  z.v[2] = from_f<T>(y.z * inv); z.v[3] = from_f<T>(y.w * inv);
-  *reinterpret_cast<uint2*>(p.out + (long)row * p.ldo + hq * D + d) = z.u;
+  *reinterpret_cast<uint2*>(p.out + (long)row * p.ldo + hq * D + d) =
+      make_uint2(pack16<T>(y.x * inv, y.y * inv), pack16<T>(y.z * inv, y.w * inv));
   if (d == 0 && p.lse) p.lse[(long)row * p.H + hq] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * 0.6931471805599453f;
 }
 
@@ -1095,6 +1140,14 @@ static Kv8Seqs kv8_seqs(const gpt_kv8_batch& b) {
   return {b.start, b.lens, b.table, b.B, b.max_pages, b.ld_table, b.rows};
 }
 
+// Heads (columns of heads) that a block of append or read takes: all of them when
+// there are blocks enough for every SM to hold eight of them even so, fewer for
+// small calls, down to one.
+static int kv8_per_block(int jobs, int n) {
+  const int groups = std::min(n, (148 * 8 * 2 + 2 * jobs - 1) / (2 * jobs));
+  return (n + groups - 1) / groups;
+}
+
 template <typename T, int KIND>
 static cudaError_t append_t(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 grid, cudaStream_t s) {
   const size_t smem = (size_t)c.page * (c.head_dim + KV8_PAD);
@@ -1203,8 +1256,10 @@ int gpt_kv8_append(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, co
   const char* why = kv8_check_call(c, layer, b, dtype, k, ldk, v, ldv, w, w);
   if (*why) return kv8_refuse("gpt_kv8_append", why);
   if (b->B == 0 || b->rows == 0) return GPT_OK;
-  Kv8AppendP p = {kv8_layer(*c, layer), kv8_seqs(*b), (const uint16_t*)k, (const uint16_t*)v, ldk, ldv, err};
-  const dim3 grid(kv8_jobs(*b, p.L.lp), c->n_kv_heads, 2);
+  Kv8AppendP p = {kv8_layer(*c, layer), kv8_seqs(*b), (const uint16_t*)k, (const uint16_t*)v, ldk, ldv, 0, err};
+  const int jobs = kv8_jobs(*b, p.L.lp);
+  p.heads = kv8_per_block(jobs, c->n_kv_heads);
+  const dim3 grid(jobs, (c->n_kv_heads + p.heads - 1) / p.heads, 2);
   cudaStream_t s = (cudaStream_t)stream;
   const bool i8 = c->kind == GPT_KV8_INT8;
   ++g_kernel_launches;
@@ -1220,8 +1275,10 @@ int gpt_kv8_read(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, void
   const char* why = kv8_check_call(c, layer, b, dtype, k, ldk, v, ldv, w, w);
   if (*why) return kv8_refuse("gpt_kv8_read", why);
   if (b->B == 0 || b->rows == 0) return GPT_OK;
-  Kv8ReadP p = {kv8_layer(*c, layer), kv8_seqs(*b), (uint16_t*)k, (uint16_t*)v, ldk, ldv, err};
-  const dim3 grid(kv8_jobs(*b, 4), (unsigned)((w + 127) / 128), 2);
+  Kv8ReadP p = {kv8_layer(*c, layer), kv8_seqs(*b), (uint16_t*)k, (uint16_t*)v, ldk, ldv, 0, err};
+  const int jobs = kv8_jobs(*b, 4), cols = (int)((w + 127) / 128);
+  p.cols = kv8_per_block(jobs, cols);
+  const dim3 grid(jobs, (cols + p.cols - 1) / p.cols, 2);
   cudaStream_t s = (cudaStream_t)stream;
   const bool i8 = c->kind == GPT_KV8_INT8;
   ++g_kernel_launches;

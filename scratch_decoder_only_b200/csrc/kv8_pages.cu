@@ -2,23 +2,28 @@
 // compacting them, all decided on the device (include/gpt.h).
 //
 // Free pages are the zeros of ref[n_pages]; a request takes the k-th lowest
-// one.  One cluster of eight blocks reads ref twice, each block a slice: first
-// it counts the zeros, the counts meet in distributed shared memory, then it
-// ranks them and hands page number k to the request of that rank, found by
-// bisection in the requests' running sums.  Every launch reads the whole of
-// ref (4 bytes a page; a pool of 100,000 pages is 0.4 MB in L2) and nothing
-// depends on an earlier call, so any table that a host writes is as good as one
-// that these kernels made.  What bounds them is latency: the launch, the
-// barriers between the phases and the two trips to memory, not the bytes.
+// one.  One cluster of eight blocks reads ref once to count the zeros of every
+// 1024 pages, the blocks in turn (the lowest pages are wanted, so slices would
+// leave the first block with all the work); the counts meet through distributed
+// shared memory, and the pages whose ranks are wanted are looked at again: page
+// number k goes to the request of that rank, found by bisection in the requests'
+// running sums.  Every launch reads the whole of ref (4 bytes a page; a pool of
+// 100,000 pages is 0.4 MB in L2) and nothing depends on an earlier call, so any
+// table that a host writes is as good as one that these kernels made.  What
+// bounds them is latency: the launch, the barriers between the phases and the
+// trips to memory, not the bytes.
 #include <cooperative_groups.h>
+#include <algorithm>
 #include <string>
+#include <utility>
 #include "kv8.cuh"
 
 namespace cg = cooperative_groups;
 
 #define KVP_CTAS 8
 #define KVP_THREADS 1024
-#define KVP_MAX 16384   // requests a call
+#define KVP_MAX 16384        // requests a call
+#define KVP_PAGES (1 << 24)   // pages of a pool
 
 struct Kv8PoolP {
   int *table, *lens, *ref;
@@ -82,7 +87,7 @@ __device__ __forceinline__ int cluster_sum(cg::cluster_group& cl, int* slot, int
 
 // FORK = false: request i grows row i by add[i].  FORK = true: request i makes
 // row dst[i] a copy of row src[i].  Both need pages; fork's copies of them
-// follow in kvp_copy_kernel.
+// follow in kvp_fork_copy_kernel.
 //
 // Forks to the same row: the claims are negative numbers put into lens[dst]
 // (0 while empty) with a minimum, so the first pair wins whatever the order of
@@ -93,95 +98,128 @@ __global__ void __cluster_dims__(KVP_CTAS, 1, 1) __launch_bounds__(KVP_THREADS)
                     int n, int* __restrict__ done) {
   griddep_wait();
   griddep_release();
-  extern __shared__ int first[];   // [n + 1] running sum of the pages needed
-  __shared__ int wsum[32], slot, sflag;
+  // [n + 1] running sum of the pages needed, [n] the place in the row of a request's first page, [chunks] free
+  // pages of each 1024, then those before it
+  extern __shared__ int first[];
+  __shared__ int wsum[32], sflag;
   cg::cluster_group cl = cg::this_cluster();
-  const int rank = cl.block_rank(), tid = threadIdx.x;
-  const int P1 = (1 << p.lp) - 1, claim0 = -0x7fffffff;
-  if (FORK) {
-    if (rank == 0) {
-      for (int i = tid; i < n; i += KVP_THREADS) {
-        const int a = src[i], z = dst[i];
-        first[i] = (unsigned)a < (unsigned)p.n_rows && (unsigned)z < (unsigned)p.n_rows && p.lens[z] == 0;
-      }
-      __syncthreads();
-      for (int i = tid; i < n; i += KVP_THREADS)
-        if (first[i]) atomicMin(&p.lens[dst[i]], claim0 + i);
-      __threadfence();
+  const int rank = cl.block_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P1 = (1 << p.lp) - 1, claim0 = -0x7fffffff, chunks = (p.n_pages + KVP_THREADS - 1) / KVP_THREADS;
+  int *place = first + n + 1, *chunk = place + n;
+  // ---- free pages of this block's chunks, the loads ahead of everything else
+  for (int c = rank + tid * KVP_CTAS; c < chunks; c += KVP_CTAS * KVP_THREADS) chunk[c] = 0;
+  __syncthreads();
+  for (int c0 = rank; c0 < chunks; c0 += 8 * KVP_CTAS) {
+    int r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int id = (c0 + i * KVP_CTAS) * KVP_THREADS + tid;
+      r[i] = id < p.n_pages ? p.ref[id] : 1;   // (n_pages <= 2^24: no overflow)
     }
-    cl.sync();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const unsigned m = __ballot_sync(0xffffffffu, r[i] <= 0);
+      if (lane == 0 && m) atomicAdd(&chunk[c0 + i * KVP_CTAS], __popc(m));
+    }
   }
+  if (FORK && rank == 0) {
+    for (int i = tid; i < n; i += KVP_THREADS) {
+      const int a = src[i], z = dst[i];
+      first[i] = (unsigned)a < (unsigned)p.n_rows && (unsigned)z < (unsigned)p.n_rows && p.lens[z] == 0;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += KVP_THREADS)
+      if (first[i]) atomicMin(&p.lens[dst[i]], claim0 + i);
+    __threadfence();
+  }
+  cl.sync();   // counts and claims are there
+  for (int c = tid; c < chunks; c += KVP_THREADS)
+    if (c % KVP_CTAS != rank) chunk[c] = *cl.map_shared_rank(chunk + c, c % KVP_CTAS);
+  auto gathered = cl.barrier_arrive();
   // ---- pages that each request needs (an invalid one: none)
   int carry = 0;
   bool bad_pos = false;
   for (int i0 = 0; i0 < n; i0 += KVP_THREADS) {
     const int i = i0 + tid;
-    int need = 0;
+    int need = 0, at = 0;
     if (i < n) {
       if (FORK) {
         const int z = dst[i], a = src[i];
         if ((unsigned)z < (unsigned)p.n_rows && (unsigned)a < (unsigned)p.n_rows && p.lens[z] == claim0 + i) {
           const int len = p.lens[a];
-          need = len > 0 && (len & P1) && ((len - 1) >> p.lp) < p.max_pages;
+          at = max(len, 0) >> p.lp;
+          need = len > 0 && (len & P1) && at < p.max_pages;
         }
       } else {
         const int len = p.lens[i], ad = add[i];
         const long want = (long)len + ad;
-        if (ad < 0 || len < 0 || want > ((long)p.max_pages << p.lp)) bad_pos = true;
-        else need = (int)((want + P1) >> p.lp) - ((len + P1) >> p.lp);
+        if (ad < 0 || len < 0 || want > ((long)p.max_pages << p.lp)) {
+          bad_pos = true;
+        } else {
+          at = (len + P1) >> p.lp;
+          need = (int)((want + P1) >> p.lp) - at;
+        }
       }
     }
     int tot;
     const int ex = block_scan(need, wsum, tot);
-    if (i < n) first[i] = carry + ex;
+    if (i < n) {
+      first[i] = carry + ex;
+      place[i] = at;
+    }
     carry += tot;
   }
   if (tid == 0) first[n] = carry;
   if (bad_pos && rank == 0) set_dev_err(p.err, GPT_DEVERR_POS);
   __syncthreads();
   const int total = carry;
+  cl.barrier_wait(std::move(gathered));   // the blocks have each other's counts: they may be overwritten
 
-  // ---- free pages of the slice, and of the slices before
   int avail = 0x7fffffff;
   if (total > 0) {
-    const Slice sl = kvp_slice(p.n_pages, rank);
-    int cnt = 0;
-    for (int i = sl.a + 4 * tid; i < sl.b; i += 4 * KVP_THREADS) cnt += __popc(kvp_mask(p.ref, i, sl.b, false));
-    int mine;
-    block_scan(cnt, wsum, mine);
-    int base = cluster_sum(cl, &slot, mine, avail);
-    // ---- rank them; page number k of the pool goes to the request that holds rank k
-    for (int i0 = sl.a; i0 < sl.b && base < total; i0 += 4 * KVP_THREADS) {
-      const int i = i0 + 4 * tid;
-      unsigned m = i < sl.b ? kvp_mask(p.ref, i, sl.b, false) : 0u;
+    // ---- free pages before each chunk, and in all
+    avail = 0;
+    for (int c0 = 0; c0 < chunks; c0 += KVP_THREADS) {
+      const int c = c0 + tid;
       int tot;
-      int k = base + block_scan(__popc(m), wsum, tot);
-      for (; m && k < total; m &= m - 1, ++k) {
-        const int id = i + __ffs(m) - 1;
-        int lo = 0, hi = n - 1;   // the last request with first <= k
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (first[mid] <= k) lo = mid;
-          else hi = mid - 1;
-        }
-        if (first[lo + 1] > avail) break;   // not served: no later rank is either
-        const int r = FORK ? dst[lo] : lo;
-        const int len = FORK ? p.lens[src[lo]] : p.lens[lo];
-        const int at = (FORK ? len >> p.lp : (len + P1) >> p.lp) + k - first[lo];
-        p.table[(long)r * p.ld_table + at] = id;
-        p.ref[id] = 1;
+      const int ex = block_scan(c < chunks ? chunk[c] : 0, wsum, tot);
+      if (c < chunks) chunk[c] = avail + ex;
+      avail += tot;
+    }
+    __syncthreads();
+    // ---- page number k of the pool goes to the request that holds rank k
+    for (int c = rank; c < chunks && chunk[c] < total; c += KVP_CTAS) {
+      const int id = c * KVP_THREADS + tid;
+      const bool free = id < p.n_pages && p.ref[id] <= 0;
+      const unsigned m = __ballot_sync(0xffffffffu, free);
+      __syncthreads();
+      if (lane == 0) wsum[warp] = __popc(m);
+      __syncthreads();
+      int k = chunk[c] + __popc(m & ((1u << lane) - 1));
+      // the warps before this one
+      const int w = lane < warp ? wsum[lane] : 0;
+      k += __reduce_add_sync(0xffffffffu, w);
+      if (!free || k >= total) continue;
+      int lo = 0, hi = n - 1;   // the last request with first <= k
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= k) lo = mid;
+        else hi = mid - 1;
       }
-      base += tot;
+      if (first[lo + 1] > avail) continue;   // not served
+      const int r = FORK ? dst[lo] : lo;
+      p.table[(long)r * p.ld_table + place[lo] + k - first[lo]] = id;
+      p.ref[id] = 1;
     }
   }
   // ---- whole pages of the forks: shared
   if (FORK) {
-    const int warps = KVP_CTAS * (KVP_THREADS / 32), w = rank * (KVP_THREADS / 32) + (tid >> 5), lane = tid & 31;
+    const int warps = KVP_CTAS * (KVP_THREADS / 32), w = rank * (KVP_THREADS / 32) + warp;
     for (int i = w; i < n; i += warps) {
       const int a = src[i], z = dst[i];
       if ((unsigned)a >= (unsigned)p.n_rows || (unsigned)z >= (unsigned)p.n_rows || p.lens[z] != claim0 + i) continue;
       if (first[i + 1] > first[i] && first[i + 1] > avail) continue;
-      const int full = min(max(p.lens[a], 0) >> p.lp, p.max_pages);
+      const int full = min(place[i], p.max_pages);
       for (int j = lane; j < full; j += 32) {
         const int id = p.table[(long)a * p.ld_table + j];
         p.table[(long)z * p.ld_table + j] = id;
@@ -261,7 +299,8 @@ __device__ __forceinline__ void kvp_copy_chunk(const Kv8CopyP& c, int a, int z, 
   }
 }
 
-// The part-filled last pages of the forks: one block per (chunk, pair).
+// The part-filled last pages of the forks: gridDim.x blocks per pair share its
+// layers, keys and values.
 __global__ void __launch_bounds__(256) kvp_fork_copy_kernel(Kv8PoolP p, Kv8CopyP c, const int* __restrict__ src,
                                                             const int* __restrict__ dst, const int* __restrict__ done,
                                                             int chunks) {
@@ -276,7 +315,7 @@ __global__ void __launch_bounds__(256) kvp_fork_copy_kernel(Kv8PoolP p, Kv8CopyP
     if (threadIdx.x == 0) set_dev_err(p.err, GPT_DEVERR_PAGE);
     return;
   }
-  kvp_copy_chunk(c, a, z, blockIdx.x, chunks);
+  for (int sub = blockIdx.x; sub < 2 * c.layers * chunks; sub += gridDim.x) kvp_copy_chunk(c, a, z, sub, chunks);
 }
 
 // ---- free: one block per listed row.  The exchange of the length gives the
@@ -406,7 +445,7 @@ static const char* kvp_check(const gpt_kv8_pool* p) {
   if (!p->table || !p->lens || !p->ref) return "table, lens and ref must be non-NULL";
   if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) return "page must be 16, 32, 64 or 128";
   if (p->n_rows < 1 || p->n_rows > KVP_MAX) return "n_rows out of range [1, 16384]";
-  if (p->n_pages < 1 || p->n_pages > (1 << 30)) return "n_pages out of range";
+  if (p->n_pages < 1 || p->n_pages > KVP_PAGES) return "n_pages out of range [1, 2^24]";
   if (p->max_pages < 1 || p->ld_table < p->max_pages || (long)p->max_pages * p->page > 0x7fffff00L)
     return "need 1 <= max_pages <= ld_table and max_pages * page < 2^31";
   return "";
@@ -428,10 +467,10 @@ static Kv8CopyP kvp_copy(const gpt_kv8_cache& c) {
 template <bool FORK>
 static cudaError_t kvp_grow(const Kv8PoolP& p, const int* add, const int* src, const int* dst, int n, int* done,
                             cudaStream_t s) {
-  const size_t smem = ((size_t)n + 1) * sizeof(int);
+  const size_t smem = (2 * (size_t)n + 1 + (p.n_pages + KVP_THREADS - 1) / KVP_THREADS) * sizeof(int);
   if (smem > 40000) {
     const cudaError_t e = cudaFuncSetAttribute(kvp_grow_kernel<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (KVP_MAX + 1) * (int)sizeof(int));
+                                               (2 * KVP_MAX + 1 + KVP_PAGES / KVP_THREADS) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
   }
   ++g_kernel_launches;
@@ -461,10 +500,12 @@ int gpt_kv8_fork(const gpt_kv8_pool* p, const gpt_kv8_cache* c, const int32_t* s
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = kvp_grow<true>(P, nullptr, src, dst, n, done, s);
   if (e != cudaSuccess) return kvp_done("gpt_kv8_fork", e);
-  const int chunks = (C.bytes + KVP_CHUNK - 1) / KVP_CHUNK;
+  const int chunks = (C.bytes + KVP_CHUNK - 1) / KVP_CHUNK, subs = 2 * C.layers * chunks;
+  // two waves of eight blocks an SM: a block looks its pages up once for all that it copies
+  const int share = std::max(1, std::min(subs, 148 * 16 / n));
   ++g_kernel_launches;
-  return kvp_done("gpt_kv8_fork", launch_k(kvp_fork_copy_kernel, dim3((unsigned)(2 * C.layers * chunks), n), dim3(256), 0, s, P,
-                                           C, src, dst, (const int*)done, chunks));
+  return kvp_done("gpt_kv8_fork", launch_k(kvp_fork_copy_kernel, dim3((unsigned)share, n), dim3(256), 0, s, P, C, src,
+                                           dst, (const int*)done, chunks));
 }
 
 int gpt_kv8_free(const gpt_kv8_pool* p, const int32_t* rows, int n, uint32_t* err, void* stream) {
