@@ -275,6 +275,25 @@ int gpt_sample_decode(gpt_model* m, const int32_t* prompt, int B, int Tp, int n_
 int gpt_beam_decode(gpt_model* m, const int32_t* prompt, int B, int Tp, int n_new, int width, int32_t* out,
                     float* scores);
 
+/* Parallel sampling: n_samples continuations of each prompt, drawn as in
+ * gpt_sample_decode, over a key/value cache held in 8 bits and in pages (the
+ * gpt_kv8_* calls below; kv_kind GPT_KV8_INT8 or GPT_KV8_E4M3).  A prompt is
+ * computed and stored once: its continuations share its full pages and copy the
+ * last one.  The prompt itself is computed from 16-bit keys and values, the new
+ * tokens read the 8-bit ones, so logits differ from gpt_sample_decode's by the
+ * codes' rounding.
+ *  prompt    device int32 [B, Tp]
+ *  uniforms  device float [B, n_samples, n_new], values in [0, 1)
+ *  out       device int32 [B, n_samples, n_new]
+ * The first call allocates the cache (2 * n_layers * max_batch * max_seq *
+ * n_kv_heads * head size bytes and a few), which gpt_destroy frees; it must
+ * come before any stream capture.
+ * Requires 16-bit precision, vocab <= 55000, B * n_samples <= max_batch and
+ * <= 32, Tp + n_new - 1 <= max_seq.
+ * Errors: as gpt_sample_decode; GPT_ERR_NOMEM. */
+int gpt_sample_parallel(gpt_model* m, const int32_t* prompt, int B, int Tp, int n_new, int n_samples, int kv_kind,
+                        const gpt_sampling* sp, const float* uniforms, int32_t* out);
+
 /* Number of parameters N in the canonical layout:
  *  wte[Vp,C], wpe[max_seq,C]; per layer ln1_g[C], ln1_b[C], w_qkv[3C,C]
  *  (rows: q, then k, then v; head h = rows h*d..h*d+d-1 of each), b_qkv[3C],
@@ -494,8 +513,9 @@ int gpt_kv8_read(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, void
 int gpt_kv8_attention(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, const void* q, long ldq, int n_heads,
                       int dtype, float scale, void* out, long ldo, float* lse, void* work, size_t work_bytes,
                       uint32_t* err, void* stream);
-/* Bytes of scratch that gpt_kv8_attention needs for a batch with this B, rows
- * and max_pages (its pointers are not read), on the current device. */
+/* Bytes of scratch that gpt_kv8_attention needs for a cache of this shape and a
+ * batch with this B, rows and max_pages (neither's pointers are read, but
+ * whether start is NULL), on the current device. */
 int gpt_kv8_attention_work(const gpt_kv8_cache* c, const gpt_kv8_batch* b, int n_heads, size_t* bytes);
 
 /* Which pages the rows (sequences) of a cache hold, kept on the device.

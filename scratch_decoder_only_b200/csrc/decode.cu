@@ -873,15 +873,15 @@ cudaError_t launch_step_advance(int* step, cudaStream_t s) {
 }
 
 template <typename T>
-__global__ void gather_last_kernel(const T* __restrict__ x, int Tp, int C, T* __restrict__ out) {
-  int b = blockIdx.x;
+__global__ void gather_last_kernel(const T* __restrict__ x, int Tp, int C, int copies, T* __restrict__ out) {
+  const int r = blockIdx.x, b = r / copies;
   for (int c = threadIdx.x; c < C; c += blockDim.x)
-    out[(long)b * C + c] = x[((long)b * Tp + Tp - 1) * C + c];
+    out[(long)r * C + c] = x[((long)b * Tp + Tp - 1) * C + c];
 }
 template <typename T>
-cudaError_t launch_gather_last(const T* x, int B, int Tp, int C, T* out, cudaStream_t s) {
+cudaError_t launch_gather_last(const T* x, int B, int Tp, int C, T* out, cudaStream_t s, int copies) {
   ++g_kernel_launches;
-  gather_last_kernel<T><<<B, 256, 0, s>>>(x, Tp, C, out);
+  gather_last_kernel<T><<<B * copies, 256, 0, s>>>(x, Tp, C, copies, out);
   return cudaGetLastError();
 }
 
@@ -895,7 +895,7 @@ cudaError_t launch_gather_last(const T* x, int B, int Tp, int C, T* out, cudaStr
   template cudaError_t launch_kv_fill<T>(const T*, T*, T*, int, int, int, int, const DecLayout&, cudaStream_t); \
   template cudaError_t launch_dec_attn<T>(const T*, T*, T*, T*, float*, unsigned*, int, int, int, int, int, const int*,      \
                                           const DecLayout&, cudaStream_t);                               \
-  template cudaError_t launch_gather_last<T>(const T*, int, int, int, T*, cudaStream_t);
+  template cudaError_t launch_gather_last<T>(const T*, int, int, int, T*, cudaStream_t, int);
 INSTD(float)
 INSTD(bf16)
 INSTD(f16)

@@ -99,6 +99,17 @@ struct gpt_model {
   int* dsrc = nullptr;
   float* dbcs = nullptr;
   int* dbct = nullptr;
+  // parallel sampling (gpt_sample_parallel) over the 8-bit paged cache, whose
+  // buffers are allocated by the first such call; kv8_n = 0: off
+  int kv8_n = 0;
+  char* kv8_buf = nullptr;
+  gpt_kv8_cache kv8_cache = {};
+  gpt_kv8_pool kv8_pool = {};
+  gpt_kv8_batch kv8_batch = {};    // one new token for each decode row
+  void* kv8_work = nullptr;
+  size_t kv8_work_bytes = 0;
+  int* kv8_ints = nullptr;         // the arrays of kv8_arrays
+  int dec_kv8 = 0;                 // 1 + kind the captured graph was built with
   int dec_beam_w = 0;
   float* dec_beam_scores = nullptr;
   bool dec_smp_on = false;   // the sampling state the captured graph was built with
@@ -1015,6 +1026,113 @@ static DecLayout dec_layout(const gpt_model* m) {
   return L;
 }
 
+#define CKV(x)                                               \
+  do {                                                       \
+    int r_ = (x);                                            \
+    if (r_ != GPT_OK) FAIL(r_, gpt_last_error(nullptr));     \
+  } while (0)
+
+#define KV8_PAGE 16   // tokens a page: a fork copies half of one on average
+
+// Device int arrays of the paged decode, for R = max_batch rows.
+struct Kv8Arrays {
+  int *prompt_add, *one, *prompt_lens, *start, *src, *dst, *rows, *done;
+  size_t n;
+};
+static Kv8Arrays kv8_arrays(const gpt_model* m) {
+  Kv8Arrays a;
+  int* p = m->kv8_ints;
+  const int R = m->Bmax;
+  a.prompt_add = p; p += R;
+  a.one = p; p += R;
+  a.prompt_lens = p; p += R;
+  a.start = p; p += R + 1;
+  a.src = p; p += R;
+  a.dst = p; p += R;
+  a.rows = p; p += R;
+  a.n = p - m->kv8_ints;   // what the host fills
+  a.done = p;
+  return a;
+}
+
+static int kv8_alloc(gpt_model* m) {
+  if (m->kv8_buf) return GPT_OK;
+  const int R = m->Bmax, mp = (m->Tmax + KV8_PAGE - 1) / KV8_PAGE;
+  if ((long)R * mp > (1L << 24) || R > 16384) FAIL(GPT_ERR_ARG, "max_batch * max_seq too large for the paged cache");
+  gpt_kv8_cache c = {};
+  c.n_layers = m->NL; c.n_pages = R * mp; c.n_kv_heads = m->Hkv; c.head_dim = m->d; c.page = KV8_PAGE;
+  gpt_kv8_pool p = {};
+  p.n_rows = R; p.max_pages = p.ld_table = mp; p.n_pages = c.n_pages; p.page = KV8_PAGE;
+  gpt_kv8_batch b = {};
+  b.B = b.rows = R; b.max_pages = b.ld_table = mp;
+  size_t work = 0;
+  CKV(gpt_kv8_attention_work(&c, &b, m->H, &work));
+  const size_t scales = (size_t)c.n_layers * c.n_pages * c.n_kv_heads;
+  Carver cv;
+  cv.add(&c.k, scales * KV8_PAGE * c.head_dim);
+  cv.add(&c.v, scales * KV8_PAGE * c.head_dim);
+  cv.add((void**)&c.k_scale, scales * 4);
+  cv.add((void**)&c.v_scale, scales * 4);
+  cv.add((void**)&p.table, (size_t)R * mp * 4);
+  cv.add((void**)&p.lens, (size_t)R * 4);
+  cv.add((void**)&p.ref, (size_t)c.n_pages * 4);
+  cv.add((void**)&m->kv8_ints, ((size_t)8 * R + 1) * 4);
+  cv.add(&m->kv8_work, work + 16);
+  char* buf = nullptr;
+  const cudaError_t e = cudaMalloc((void**)&buf, cv.off + 256);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    m->err = std::string("cudaMalloc of the paged cache (") + std::to_string(cv.off) + " bytes) failed: " +
+             cudaGetErrorString(e);
+    return GPT_ERR_NOMEM;
+  }
+  for (auto& it : cv.items) *it.first = buf + it.second;
+  m->kv8_buf = buf;
+  m->kv8_cache = c;
+  m->kv8_pool = p;
+  m->kv8_work_bytes = work;
+  return GPT_OK;
+}
+
+// The prompts' keys and values (of a forward pass over them) into row b n of each
+// prompt b, and the other n - 1 rows of a prompt forked from it.
+template <typename T>
+static int kv8_fill(gpt_model* m, int B, int Tp, cudaStream_t s) {
+  Acts<T> A(m);
+  const int n = m->kv8_n, R = m->Bmax;
+  const gpt_kv8_pool& P = m->kv8_pool;
+  const Kv8Arrays a = kv8_arrays(m);
+  std::vector<int> h(a.n);
+  auto at = [&](int* dev, int i) -> int& { return h[dev - m->kv8_ints + i]; };
+  int forks = 0;
+  for (int r = 0; r < R; ++r) {
+    const bool on = r < B * n;
+    at(a.prompt_add, r) = on && r % n == 0 ? Tp : 0;
+    at(a.one, r) = on;
+    at(a.prompt_lens, r) = Tp;
+    at(a.start, r) = r * Tp;
+    at(a.rows, r) = r;
+    if (on && r % n) {
+      at(a.src, forks) = r - r % n;
+      at(a.dst, forks++) = r;
+    }
+  }
+  at(a.start, R) = R * Tp;
+  CK(cudaMemcpyAsync(m->kv8_ints, h.data(), h.size() * sizeof(int), cudaMemcpyHostToDevice, s));
+  CK(cudaMemsetAsync(P.lens, 0, (size_t)R * 4, s));
+  CK(cudaMemsetAsync(P.ref, 0, (size_t)P.n_pages * 4, s));
+  unsigned* err = &m->sc->err;
+  CKV(gpt_kv8_extend(&P, a.prompt_add, err, s));
+  gpt_kv8_batch b = {};
+  b.start = a.start; b.lens = a.prompt_lens; b.table = P.table;
+  b.B = B; b.max_pages = P.max_pages; b.ld_table = n * P.ld_table; b.rows = B * Tp;
+  const int dtype = m->fp16 ? GPT_PRECISION_FP16 : GPT_PRECISION_BF16, kcol = m->C, vcol = m->C + m->Hkv * m->d;
+  for (int l = 0; l < m->NL; ++l)
+    CKV(gpt_kv8_append(&m->kv8_cache, l, &b, A.qkv(l) + kcol, m->QW, A.qkv(l) + vcol, m->QW, dtype, err, s));
+  if (forks) CKV(gpt_kv8_fork(&P, &m->kv8_cache, a.src, a.dst, forks, a.done, err, s));
+  return GPT_OK;
+}
+
 template <typename T>
 static int decode_step(gpt_model* m, int B, int Tp, int n_new, int32_t* out, cudaStream_t s) {
   Acts<T> A(m);
@@ -1040,6 +1158,8 @@ static int decode_step(gpt_model* m, int B, int Tp, int n_new, int32_t* out, cud
   // input row was embedded by the previous step's argmax (the first one by
   // decode_impl)
   const bool greedy = !m->beam_w && !m->smp_on;
+  const int kv8_dtype = m->fp16 ? GPT_PRECISION_FP16 : GPT_PRECISION_BF16;
+  if (m->kv8_n) CKV(gpt_kv8_extend(&m->kv8_pool, kv8_arrays(m).one, &m->sc->err, s));
   if (!greedy)
     CK(launch_dec_embed<T>(m->dtok, A.P(m->o_wte), ll ? nullptr : A.P(m->o_wpe), x, B, C, Tp - 1, stepc, m->Tmax,
                            &m->sc->err, s, st));
@@ -1048,8 +1168,14 @@ static int decode_step(gpt_model* m, int B, int Tp, int n_new, int32_t* out, cud
     CK(dec_ln_proj<T>(m, x, A.P(lo.ln1_g), P0(lo.ln1_b), h, B, C, A.W(lo.w_qkv), QW, P0(lo.b_qkv), nullptr, 0, q,
                       nullptr, nullptr, s, l == 0 ? st : st_f2));
     if (ll) CK(rope16<T>(q, QW, B, H, C, m->Hkv, d, nullptr, Tp - 1, stepc, m->rope_tab, m->Tmax, false, s));
-    CK(launch_dec_attn<T>(q, kc + l * kvl, vc + l * kvl, att, m->dpart, m->dacnt, B, H, d, m->Tmax, Tp - 1, stepc, DL,
-                          s));
+    if (m->kv8_n) {
+      CKV(gpt_kv8_append(&m->kv8_cache, l, &m->kv8_batch, q + DL.kcol, QW, q + DL.vcol, QW, kv8_dtype, &m->sc->err, s));
+      CKV(gpt_kv8_attention(&m->kv8_cache, l, &m->kv8_batch, q, QW, H, kv8_dtype, 1.0f / sqrtf((float)d), att, C,
+                            nullptr, m->kv8_work, m->kv8_work_bytes, &m->sc->err, s));
+    } else {
+      CK(launch_dec_attn<T>(q, kc + l * kvl, vc + l * kvl, att, m->dpart, m->dacnt, B, H, d, m->Tmax, Tp - 1, stepc,
+                            DL, s));
+    }
     CK(dec_proj<T>(m, att, B, C, A.W(lo.w_o), C, P0(lo.b_o), x, 0, x, nullptr, nullptr, s, st));
     if (ll) {
       CK(dec_ln_proj<T>(m, x, A.P(lo.ln2_g), nullptr, h, B, C, A.W(lo.w_fc), 2 * F, nullptr, nullptr, 0, u, nullptr,
@@ -1098,11 +1224,17 @@ static int decode_impl(gpt_model* m, const int32_t* prompt, int B, int Tp, int n
   m->logits_valid = false;
   size_t kvl = (size_t)m->Bmax * m->Hkv * m->Tmax * d;
   const DecLayout DL = dec_layout(m);
-  for (int l = 0; l < m->NL; ++l)
-    CK(launch_kv_fill<T>(A.qkv(l), (T*)m->kc + l * kvl, (T*)m->vc + l * kvl, B, Tp, d, m->Tmax, DL, s));
-  // first new token: from the prefill's last position
-  CK(launch_gather_last<T>((const T*)m->xf, B, Tp, C, (T*)m->dxf, s));
-  CK(dec_proj<T>(m, (const T*)m->dxf, B, C, A.W(m->o_head), m->Vp, nullptr, nullptr, 2, nullptr, nullptr,
+  if (m->kv8_n) {
+    CKI(kv8_fill<T>(m, B, Tp, s));
+  } else {
+    for (int l = 0; l < m->NL; ++l)
+      CK(launch_kv_fill<T>(A.qkv(l), (T*)m->kc + l * kvl, (T*)m->vc + l * kvl, B, Tp, d, m->Tmax, DL, s));
+  }
+  // first new token: from the prefill's last position (of each of a prompt's n
+  // samples: the same logits, a draw of its own)
+  const int per = m->kv8_n ? m->kv8_n : 1, Bl = B * per;
+  CK(launch_gather_last<T>((const T*)m->xf, B, Tp, C, (T*)m->dxf, s, per));
+  CK(dec_proj<T>(m, (const T*)m->dxf, Bl, C, A.W(m->o_head), m->Vp, nullptr, nullptr, 2, nullptr, nullptr,
                  m->dlogits, s));
   if (m->beam_w) {
     // every beam of a prompt starts from the prompt's prefill row
@@ -1112,12 +1244,23 @@ static int decode_impl(gpt_model* m, const int32_t* prompt, int B, int Tp, int n
     CK(launch_beam_merge(m->dbcs, m->dbct, B, W, m->V, Tp, m->dsrc, m->Tmax, m->beam_scores, m->dtok, out, n_new,
                          nullptr, s));
   } else if (m->smp_on)
-    CK(launch_sample(m->dlogits, B, m->V, m->Vp, m->smp_temp, m->smp_topk, m->smp_topp, m->smp_u, n_new, m->dtok, out,
+    CK(launch_sample(m->dlogits, Bl, m->V, m->Vp, m->smp_temp, m->smp_topk, m->smp_topp, m->smp_u, n_new, m->dtok, out,
                      n_new, nullptr, s));
   else
     CK(launch_argmax(m->dlogits, B, m->V, m->Vp, m->dtok, out, n_new, nullptr, s));
-  if (n_new == 1) return GPT_OK;
-  const int Bd = m->beam_w ? B * m->beam_w : B;   // decode rows
+  const int Bd = m->beam_w ? B * m->beam_w : Bl;   // decode rows
+  // the pages go back to the pool when the last token is there
+  auto done = [&]() -> int {
+    if (m->kv8_n) CKV(gpt_kv8_free(&m->kv8_pool, kv8_arrays(m).rows, Bd, &m->sc->err, s));
+    return GPT_OK;
+  };
+  if (n_new == 1) return done();
+  if (m->kv8_n) {
+    gpt_kv8_batch& b = m->kv8_batch;
+    b.start = nullptr; b.lens = m->kv8_pool.lens; b.table = m->kv8_pool.table;
+    b.B = b.rows = Bd; b.ld_table = m->kv8_pool.ld_table;
+    b.max_pages = (Tp + n_new - 1 + KV8_PAGE - 1) / KV8_PAGE;   // as the rows grow at most
+  }
   const int one = 1;
   CK(cudaMemcpyAsync(&m->sc->dec_step, &one, sizeof(int), cudaMemcpyHostToDevice, s));
   if (!m->beam_w && !m->smp_on) {
@@ -1133,7 +1276,8 @@ static int decode_impl(gpt_model* m, const int32_t* prompt, int B, int Tp, int n
   }
   const bool same_smp = m->dec_smp_on == m->smp_on && m->dec_smp_temp == m->smp_temp &&
                         m->dec_smp_topk == m->smp_topk && m->dec_smp_topp == m->smp_topp && m->dec_smp_u == m->smp_u &&
-                        m->dec_beam_w == m->beam_w && m->dec_beam_scores == m->beam_scores;
+                        m->dec_beam_w == m->beam_w && m->dec_beam_scores == m->beam_scores &&
+                        m->dec_kv8 == (m->kv8_n ? 1 + m->kv8_cache.kind : 0);
   if (!m->dec_graph || m->dec_B != Bd || m->dec_Tp != Tp || m->dec_nnew != n_new || m->dec_out != out || !same_smp) {
     if (m->dec_graph) { cudaGraphExecDestroy(m->dec_graph); m->dec_graph = nullptr; }
     cudaGraph_t g = nullptr;
@@ -1152,6 +1296,7 @@ static int decode_impl(gpt_model* m, const int32_t* prompt, int B, int Tp, int n
     m->dec_smp_on = m->smp_on; m->dec_smp_temp = m->smp_temp; m->dec_smp_topk = m->smp_topk;
     m->dec_smp_topp = m->smp_topp; m->dec_smp_u = m->smp_u;
     m->dec_beam_w = m->beam_w; m->dec_beam_scores = m->beam_scores;
+    m->dec_kv8 = m->kv8_n ? 1 + m->kv8_cache.kind : 0;
   }
   CK(cudaEventRecord(m->ev_a, s));
   CK(cudaStreamWaitEvent(m->cap_stream, m->ev_a, 0));
@@ -1159,7 +1304,7 @@ static int decode_impl(gpt_model* m, const int32_t* prompt, int B, int Tp, int n
   g_kernel_launches += (unsigned long long)m->dec_kernels * (n_new - 1);
   CK(cudaEventRecord(m->ev_b, m->cap_stream));
   CK(cudaStreamWaitEvent(s, m->ev_b, 0));
-  return GPT_OK;
+  return done();
 }
 
 // ---------------------------------------------------------------------------
@@ -1269,6 +1414,7 @@ void gpt_destroy(gpt_model* m) {
   if (m->ev_a) cudaEventDestroy(m->ev_a);
   if (m->ev_b) cudaEventDestroy(m->ev_b);
   if (m->cap_stream) cudaStreamDestroy(m->cap_stream);
+  if (m->kv8_buf) cudaFree(m->kv8_buf);
   if (m->arena) cudaFree(m->arena);
   delete m;
 }
@@ -1525,6 +1671,35 @@ int gpt_beam_decode(gpt_model* m, const int32_t* prompt, int B, int Tp, int n_ne
                 : m->lp ? decode_impl<bf16>(m, prompt, B, Tp, n_new, out) : decode_impl<float>(m, prompt, B, Tp, n_new, out);
   m->beam_w = 0;
   m->beam_scores = nullptr;
+  return r;
+}
+
+int gpt_sample_parallel(gpt_model* m, const int32_t* prompt, int B, int Tp, int n_new, int n_samples, int kv_kind,
+                        const gpt_sampling* sp, const float* uniforms, int32_t* out) {
+  if (!m) return GPT_ERR_ARG;
+  m->err.clear();
+  if (!prompt || !out || !sp || !uniforms) FAIL(GPT_ERR_ARG, "prompt / out / sampling / uniforms is NULL");
+  if (!m->lp) FAIL(GPT_ERR_ARG, "the 8-bit cache needs 16-bit precision");
+  if (kv_kind != GPT_KV8_INT8 && kv_kind != GPT_KV8_E4M3) FAIL(GPT_ERR_ARG, "unknown cache kind");
+  if (!(sp->temperature >= 0.f) || sp->top_k < 0 || !(sp->top_p > 0.f && sp->top_p <= 1.f))
+    FAIL(GPT_ERR_ARG, "need temperature >= 0, top_k >= 0, 0 < top_p <= 1");
+  if (m->V > SMP_MAX_VOCAB) FAIL(GPT_ERR_ARG, "vocabulary too large for the sampling kernel");
+  if (B < 1 || n_samples < 1 || (long)B * n_samples > m->Bmax || (long)B * n_samples > 32)
+    FAIL(GPT_ERR_ARG, "B * n_samples out of range [1, min(max_batch, 32)]");
+  if (Tp < 1 || n_new < 1) FAIL(GPT_ERR_ARG, "Tp and n_new must be >= 1");
+  if ((long)Tp + n_new - 1 > m->Tmax) FAIL(GPT_ERR_STATE, "Tp + n_new - 1 exceeds max_seq");
+  CKI(kv8_alloc(m));
+  m->have_targets = false;
+  m->kv8_cache.kind = kv_kind;
+  m->kv8_n = n_samples;
+  m->smp_on = true;
+  m->smp_temp = sp->temperature;
+  m->smp_topk = sp->top_k;
+  m->smp_topp = sp->top_p;
+  m->smp_u = uniforms;
+  const int r = m->fp16 ? decode_impl<f16>(m, prompt, B, Tp, n_new, out) : decode_impl<bf16>(m, prompt, B, Tp, n_new, out);
+  m->smp_on = false;
+  m->kv8_n = 0;
   return r;
 }
 

@@ -1089,7 +1089,7 @@ __global__ void __launch_bounds__(KV8_MERGE) kv8_attn_merge_kernel(Kv8AttnP p) {
 // ---------------------------------------------------------------------------
 // Entry points
 // ---------------------------------------------------------------------------
-const char* kv8_check_cache(const gpt_kv8_cache* c) {
+static const char* kv8_check_shape(const gpt_kv8_cache* c) {
   if (!c) return "cache is NULL";
   if (c->kind != GPT_KV8_INT8 && c->kind != GPT_KV8_E4M3) return "unknown cache kind";
   if (c->n_layers < 1 || c->n_pages < 1 || c->n_kv_heads < 1 || c->n_kv_heads > 1024)
@@ -1099,6 +1099,11 @@ const char* kv8_check_cache(const gpt_kv8_cache* c) {
   if (c->head_dim != 16 && c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128)
     return "head_dim must be 16, 32, 64 or 128";
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return "page must be 16, 32, 64 or 128";
+  return "";
+}
+const char* kv8_check_cache(const gpt_kv8_cache* c) {
+  const char* why = kv8_check_shape(c);
+  if (*why) return why;
   if (!c->k || !c->v || !c->k_scale || !c->v_scale) return "cache buffers must be non-NULL";
   if (((uintptr_t)c->k | (uintptr_t)c->v) & 15) return "k and v of the cache must be 16-byte aligned";
   if (((uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 3) return "scales must be 4-byte aligned";
@@ -1291,7 +1296,7 @@ int gpt_kv8_read(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, void
 }
 
 static const char* kv8_check_heads(const gpt_kv8_cache* c, const gpt_kv8_batch* b, int H) {
-  const char* why = kv8_check_cache(c);
+  const char* why = kv8_check_shape(c);
   if (*why) return why;
   if (H < 1 || H % c->n_kv_heads) return "n_heads must be a positive multiple of n_kv_heads";
   if (!b || b->B < 0 || b->rows < 0 || b->max_pages < 1) return "need a batch with B >= 0, rows >= 0, max_pages >= 1";

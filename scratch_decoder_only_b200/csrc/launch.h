@@ -229,8 +229,9 @@ cudaError_t launch_step_advance(int* step, cudaStream_t s);
 cudaError_t launch_sample(const float* logits, int B, int V, int Vp, float temp, int top_k, float top_p,
                           const float* uni, int u_ld, int* tok, int32_t* out, int out_ld, const int* step,
                           cudaStream_t s);
+// out row b * copies + i = the last row of sequence b
 template <typename T>
-cudaError_t launch_gather_last(const T* x, int B, int Tp, int C, T* out, cudaStream_t s);
+cudaError_t launch_gather_last(const T* x, int B, int Tp, int C, T* out, cudaStream_t s, int copies = 1);
 
 // ---- decode_mma.cu: decode projections of 1-32 rows on mma.sync (16-bit T),
 // same modes and outputs as the GEMV (0: + bias + residual, 1: + bias and

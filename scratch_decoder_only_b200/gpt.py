@@ -32,7 +32,7 @@ EXPORTED = [
     "gpt_gemm_bf16_splitk_noalloc", "gpt_noalloc_status", "gpt_set_lr_schedule", "gpt_train_steps",
     "gpt_sample_decode", "gpt_backward_accumulate", "gpt_set_loss_weight", "gpt_beam_decode", "gpt_train_step",
     "gpt_kv8_append", "gpt_kv8_read", "gpt_kv8_attention", "gpt_kv8_attention_work", "gpt_kv8_extend",
-    "gpt_kv8_fork", "gpt_kv8_free", "gpt_kv8_compact",
+    "gpt_kv8_fork", "gpt_kv8_free", "gpt_kv8_compact", "gpt_sample_parallel",
 ]
 
 
@@ -136,6 +136,7 @@ def load_library(path: str = LIB_PATH):
         "gpt_noalloc_status": ([P], I),
         "gpt_set_lr_schedule": ([H, ctypes.POINTER(gpt_lr_schedule)], I),
         "gpt_sample_decode": ([H, P, I, I, I, ctypes.POINTER(gpt_sampling), P, P], I),
+        "gpt_sample_parallel": ([H, P, I, I, I, I, I, ctypes.POINTER(gpt_sampling), P, P], I),
         "gpt_beam_decode": ([H, P, I, I, I, I, P, P], I),
         "gpt_train_steps": ([H, P, P, P, I, I, I, ctypes.POINTER(gpt_adamw), P, P, P], I),
         "gpt_train_step": ([H, P, P, P, I, I, ctypes.POINTER(gpt_adamw), P, P, P], I),
@@ -322,6 +323,23 @@ class GPT:
         self._sync_stream()
         self._check(self.lib.gpt_sample_decode(self.h, _ptr(prompt), B, Tp, n_new, ctypes.byref(sp), _ptr(uniforms),
                                                _ptr(out)))
+        return out
+
+    def sample_parallel(self, prompt, n_new, n_samples, uniforms, temperature=1.0, top_k=0, top_p=1.0, kind="int8",
+                        out=None):
+        """n_samples continuations of each prompt over an 8-bit paged cache
+        (kind "int8" or "e4m3"); uniforms: device float32 [B, n_samples, n_new]
+        in [0, 1).  Returns int32 [B, n_samples, n_new]."""
+        B, Tp = prompt.shape
+        if kind not in ("int8", "e4m3"):
+            raise ValueError("kind must be int8 or e4m3")
+        if out is None:
+            out = self.torch.empty((B, n_samples, n_new), dtype=self.torch.int32, device=prompt.device)
+        sp = gpt_sampling(temperature=temperature, top_k=top_k, top_p=top_p)
+        self._sync_stream()
+        self._check(self.lib.gpt_sample_parallel(self.h, _ptr(prompt), B, Tp, n_new, n_samples,
+                                                 GPT_KV8_E4M3 if kind == "e4m3" else GPT_KV8_INT8, ctypes.byref(sp),
+                                                 _ptr(uniforms), _ptr(out)))
         return out
 
     def beam_decode(self, prompt, n_new, width):
