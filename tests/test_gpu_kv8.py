@@ -274,7 +274,7 @@ def check(torch, s, qf, out, lse, lens, new, dtype, scale=None, skip=()):
         assert np.array_equal(np.isinf(gl), np.isinf(e)), i
         fin = np.isfinite(e)
         lim = (s.d + 8) * 2.0 ** -24 * dot + 2.0 ** -21 + (n + 64) * 2.0 ** -24 + 2.0 ** -22 * np.abs(np.where(fin, e, 0))
-        assert np.all(np.abs(gl - e)[fin] <= lim[fin]), i
+        assert np.all(np.abs(gl[fin] - e[fin]) <= lim[fin]), i
 
 
 def test_attention_long_split(torch):
@@ -290,6 +290,59 @@ def test_attention_long_split(torch):
     out, lse = s.cache.attention(0, q.cuda(), s.batch(torch), return_lse=True)
     check(torch, s, qf, out, lse, lens, new, "fp16")
     assert s.cache.status() == 0
+
+
+@pytest.mark.parametrize("kind,dtype,heads,G,d,page,lens,new", [
+    ("int8", "bf16", 1, 1, 16, 16, [2500], [1]), ("e4m3", "fp16", 2, 3, 32, 32, [1300, 700], [1, 1]),
+    ("int8", "fp16", 1, 16, 64, 16, [3000, 40], [1, 1]), ("e4m3", "bf16", 1, 16, 128, 64, [1500, 641], [1, 1]),
+    ("int8", "bf16", 2, 4, 32, 64, [900, 1200], [9, 6]), ("e4m3", "bf16", 1, 5, 16, 128, [2000, 0, 77], [8, 0, 5]),
+    ("int8", "fp16", 1, 2, 128, 16, [1100], [40])])
+def test_attention_long_at_every_width(torch, kind, dtype, heads, G, d, page, lens, new):
+    """Runs of tiles that cut jobs, for 8 and for 16 queries a job."""
+    s = Setup(torch, kind, heads, d, page, lens, new, seed=G * d + page)
+    q, qf = values(torch, s.rng, (sum(new), heads * G, d), dtype, 1.5)
+    b = s.batch(torch, new != [1] * len(new))
+    out, lse = s.cache.attention(0, q.cuda(), b, return_lse=True)
+    check(torch, s, qf, out, lse, lens, new, dtype)
+    assert torch.equal(s.cache.attention(0, q.cuda(), b), out)
+    assert s.cache.status() == 0
+
+
+@pytest.mark.parametrize("top,ragged", [(90, False), (90, True), (700, True), (700, False)])
+def test_many_sequences(torch, top, ragged):
+    """More sequences than threads of a block, empty ones and ones without rows
+    among them, for whole jobs (rows of at most 512 tokens) and for runs; also append and read."""
+    rng = np.random.default_rng(top + ragged)
+    B, heads, d, P = 300, 2, 32, 16
+    lens = [int(n) for n in np.where(rng.random(B) < 0.1, 0, np.exp(rng.uniform(0, np.log(top), B)).astype(int))]
+    lens[7] = top
+    new = [min(n, int(rng.integers(0, 4))) for n in lens] if ragged else [1] * B
+    if ragged:
+        new[0], new[-1] = 0, 0
+    s = Setup(torch, "int8", heads, d, P, lens, new, seed=3)
+    q, qf = values(torch, s.rng, (sum(new), heads * 2, d), "fp16")
+    out, lse = s.cache.attention(0, q.cuda(), s.batch(torch, ragged), return_lse=True)
+    check(torch, s, qf, out, lse, lens, new, "fp16")
+    x, xf = values(torch, s.rng, (sum(new), heads, d), "fp16")
+    s.cache.status()
+    s.cache.append(0, x.cuda(), x.cuda(), s.batch(torch, ragged))
+    at = starts(new)
+    for i in range(B):
+        m = min(new[i], lens[i])
+        s.ref.append(s.table[i], lens[i], (xf[at[i + 1] - m:at[i + 1]],) * 2)
+    s.same(torch, lens)
+    assert s.cache.status() == (0 if ragged else 16)      # a row for an empty sequence has no place
+    k, v = s.cache.read(0, s.batch(torch, True, new=lens), torch.float16)
+    want = np.concatenate([s.ref.tokens(1, s.table[i], lens[i]) for i in range(B)])
+    assert np.all(np.abs(v.double().cpu().numpy() - want) <= np.abs(want) * (2.0 ** -11 + 2.0 ** -23) + 2.0 ** -25)
+
+
+def test_attention_of_equal_weights(torch):
+    """scale = 0: the mean of the values, whatever the keys."""
+    s = Setup(torch, "int8", 2, 64, 16, [100, 700], [1, 1], seed=5)
+    q, qf = values(torch, s.rng, (2, 4, 64), "bf16")
+    out, lse = s.cache.attention(0, q.cuda(), s.batch(torch, False), scale=0.0, return_lse=True)
+    check(torch, s, qf, out, lse, [100, 700], [1, 1], "bf16", scale=0.0)
 
 
 def test_attention_strides_scale_and_rows_outside(torch):
