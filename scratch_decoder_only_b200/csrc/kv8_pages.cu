@@ -275,28 +275,35 @@ struct Kv8CopyP {
 };
 #define KVP_CHUNK 16384   // bytes a block copies: 256 threads x 4 vectors of 16
 
-// One chunk of one layer's keys or values of a page (sub = ((layer * 2 + is_v) *
-// chunks + chunk)); the first chunk takes the scales along.  Four 16-byte
-// loads are in flight per thread, so that a few blocks per SM cover HBM's latency.
-__device__ __forceinline__ void kvp_copy_chunk(const Kv8CopyP& c, int a, int z, int sub, int chunks) {
+// A copy of up to KVP_CHUNK bytes by 256 threads, in two halves, so that the next
+// one's loads are under way while this one's stores are issued.
+struct KvpChunk {
+  uint4 r[4];
+  uint4* to;
+  int n;   // vectors
+};
+// Chunk `sub` = (layer * 2 + is_v) * chunks + chunk of page a, to go to page z; the
+// first chunk takes the scales along.
+__device__ __forceinline__ void kvp_load(KvpChunk& k, const Kv8CopyP& c, int a, int z, int sub, int chunks) {
   const int chunk = sub % chunks, lv = sub / chunks, layer = lv >> 1;
   const bool is_v = lv & 1;
   const long pa = (long)layer * c.layer_pages + a, pz = (long)layer * c.layer_pages + z;
   uint8_t* x = is_v ? c.v : c.k;
-  const uint4* from = reinterpret_cast<const uint4*>(x + pa * c.bytes + (long)chunk * KVP_CHUNK);
-  uint4* to = reinterpret_cast<uint4*>(x + pz * c.bytes + (long)chunk * KVP_CHUNK);
-  const int n = min(c.bytes - chunk * KVP_CHUNK, KVP_CHUNK) / 16;
-  uint4 r[4];
+  const uint4* from = reinterpret_cast<const uint4*>(x + pa * c.bytes + (long)chunk * KVP_CHUNK) + threadIdx.x;
+  k.to = reinterpret_cast<uint4*>(x + pz * c.bytes + (long)chunk * KVP_CHUNK) + threadIdx.x;
+  k.n = (min(c.bytes - chunk * KVP_CHUNK, KVP_CHUNK) / 16 - (int)threadIdx.x + 255) / 256;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (threadIdx.x + 256 * j < n) r[j] = from[threadIdx.x + 256 * j];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (threadIdx.x + 256 * j < n) to[threadIdx.x + 256 * j] = r[j];
+    if (j < k.n) k.r[j] = from[256 * j];
   if (chunk == 0) {
     float* s = is_v ? c.vs : c.ks;
     for (int h = threadIdx.x; h < c.Hkv; h += 256) s[pz * c.Hkv + h] = s[pa * c.Hkv + h];
   }
+}
+__device__ __forceinline__ void kvp_store(const KvpChunk& k) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < k.n) k.to[256 * j] = k.r[j];
 }
 
 // The part-filled last pages of the forks: gridDim.x blocks per pair share its
@@ -315,7 +322,14 @@ __global__ void __launch_bounds__(256) kvp_fork_copy_kernel(Kv8PoolP p, Kv8CopyP
     if (threadIdx.x == 0) set_dev_err(p.err, GPT_DEVERR_PAGE);
     return;
   }
-  for (int sub = blockIdx.x; sub < 2 * c.layers * chunks; sub += gridDim.x) kvp_copy_chunk(c, a, z, sub, chunks);
+  const int subs = 2 * c.layers * chunks;
+  KvpChunk now, next;
+  if (blockIdx.x < subs) kvp_load(now, c, a, z, blockIdx.x, chunks);
+  for (int sub = blockIdx.x; sub < subs; sub += gridDim.x) {
+    if (sub + gridDim.x < subs) kvp_load(next, c, a, z, sub + gridDim.x, chunks);
+    kvp_store(now);
+    now = next;
+  }
 }
 
 // ---- free: one block per listed row.  The exchange of the length gives the
@@ -416,14 +430,20 @@ __global__ void __launch_bounds__(256) kvp_move_kernel(Kv8PoolP p, Kv8CopyP c, c
   }
   const int per = 2 * c.layers * chunks;
   const long jobs = (long)moves * per;
-  for (long i = blockIdx.x; i < jobs; i += gridDim.x) {
-    const int k = (int)(i / per), sub = (int)(i % per);
-    const int a = from[k], z = to[k];
+  KvpChunk now, next;
+  auto load = [&](KvpChunk& k, long i) {
+    const int m = (int)(i / per), sub = (int)(i % per), a = from[m], z = to[m];
     if (sub == 0 && threadIdx.x == 0) {
       p.ref[z] = p.ref[a];
       p.ref[a] = 0;
     }
-    kvp_copy_chunk(c, a, z, sub, chunks);
+    kvp_load(k, c, a, z, sub, chunks);
+  };
+  if (blockIdx.x < jobs) load(now, blockIdx.x);
+  for (long i = blockIdx.x; i < jobs; i += gridDim.x) {
+    if (i + gridDim.x < jobs) load(next, i + gridDim.x);
+    kvp_store(now);
+    now = next;
   }
 }
 
