@@ -344,13 +344,13 @@ __global__ void __launch_bounds__(128) kv8_read_kernel(Kv8ReadP p) {
 // equal run of units.  A job that a run cuts leaves fp32 partials in scratch,
 // two at most per run, and a second kernel merges them in a fixed order, its
 // columns spread over the warps whose runs have a piece.  Where the host knows
-// that jobs are short (KV8_WHOLE tiles at most), a block takes a whole job, its
-// four warps the tiles in turn, and merges it in shared memory: one kernel.
+// that rows are short (KV8_WHOLE tokens at most), a block takes a whole job, its
+// four or eight warps the tiles in turn, and merges it in shared memory.
 // ---------------------------------------------------------------------------
-#define KV8_NW 4       // warps a block; KV8_WIDE where blocks take whole jobs and are few
-#define KV8_WIDE 8
-#define KV8_WHOLE 8
-#define KV8_OVER 2
+#define KV8_NW 4       // warps of a block that takes runs, or a whole job
+#define KV8_WIDE 8     // of one that takes a whole job where jobs are few
+#define KV8_WHOLE 1024 // tokens
+#define KV8_OVER 4
 
 struct Kv8AttnP {
   Kv8Layer L;
@@ -512,18 +512,25 @@ __device__ __forceinline__ bool kv8_locate(const Kv8AttnP& p, int runs, int run0
   return true;
 }
 
-template <int D>
+// 64 tokens; 32 where 128 channels of 16 queries fill the registers, and for 128
+// channels where a block takes a whole job: more warps for few tokens.  NW: warps
+// of blocks that take whole jobs (0: blocks of KV8_NW warps take runs).
+__host__ __device__ constexpr int kv8_tile(int D, int nt, bool whole) { return D == 128 && (nt == 2 || whole) ? 32 : 64; }
+template <int D, int NT, bool WHOLE>
 struct Kv8Tile {
-  static constexpr int TILE = D == 128 ? 32 : 64;
+  static constexpr int TILE = kv8_tile(D, NT, WHOLE);
   static constexpr int HALF = TILE * D;   // bytes of a tile's keys, and of its values
 };
-// NW: warps a block that takes whole jobs (0: blocks of KV8_NW warps take runs)
 template <int D, int NT, int NW>
 constexpr size_t kv8_attn_smem() {
-  return (size_t)(NW ? NW : KV8_NW) * 2 * Kv8Tile<D>::HALF + (size_t)(NW / 2) * 8 * NT * (D + 4) * 4;
+  return (size_t)(NW ? NW : KV8_NW) * 2 * Kv8Tile<D, NT, NW != 0>::HALF + (size_t)(NW / 2) * 8 * NT * (D + 4) * 4;
 }
-// Blocks of KV8_NW warps an SM holds: what their registers allow (128, 168 and 255 a thread).
-__host__ __device__ constexpr int kv8_resident(int D, int nt) { return nt == 1 ? 4 : D < 128 ? 3 : 2; }
+// Blocks an SM holds by their registers: of four warps 128, 168 or 255 a thread, of
+// eight 128 (255 where 16 queries of 128 channels need them).
+__host__ __device__ constexpr int kv8_resident(int D, int nt, int nw) {
+  return nw == KV8_WIDE ? (nt == 2 && D == 128 ? 1 : 2)
+                        : nt == 1 && (D < 128 || nw) ? 4 : nt == 1 || D < 128 ? 3 : 2;
+}
 
 // The result of query q0 + n of a job, four channels from d on.
 template <typename T>
@@ -537,11 +544,11 @@ __device__ __forceinline__ void kv8_out(const Kv8AttnP& p, int s0, int h, int qi
 }
 
 template <typename T, int D, int NT, int KIND, int NW>
-__global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT) * KV8_NW / (NW ? NW : KV8_NW))
+__global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, NW))
     kv8_attn_kernel(Kv8AttnP p) {
   constexpr bool WHOLE = NW != 0;
   constexpr int WARPS = WHOLE ? NW : KV8_NW;
-  constexpr int NQ = 8 * NT, KW = D / 16, TILE = Kv8Tile<D>::TILE, HALF = Kv8Tile<D>::HALF;
+  constexpr int NQ = 8 * NT, KW = D / 16, TILE = Kv8Tile<D, NT, WHOLE>::TILE, HALF = Kv8Tile<D, NT, WHOLE>::HALF;
   constexpr int TQ = TILE / 4;                         // tokens of a quarter
   constexpr int KP = D / 4 < 16 ? D / 4 : 16, KT = D / 4 / KP;   // bytes of a key read, reads of a quarter key
   constexpr int STEP = WHOLE ? WARPS : 1;
@@ -1179,8 +1186,9 @@ struct Kv8Plan {
 // a sequence on average: from 19 on (mean 12, one to five rows of four heads: 48
 // us with 8, 61 with 16).  Jobs of 32 queries were no faster than two of 16.
 //
-// Blocks: as many as are resident at once, or one per job where no job has more
-// than KV8_WHOLE tiles; those have twice the warps where they leave SMs idle.
+// Blocks: as many as are resident at once, or one per job where no row has room
+// for more than KV8_WHOLE tokens; those have twice the warps where two an SM are
+// enough (one sequence of 512 tokens and 12 heads: 5.9 us, 6.6 with four warps).
 static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
   static int sms = 0;
   if (!sms) {
@@ -1192,19 +1200,21 @@ static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
       cudaGetLastError();
   }
   Kv8Plan P = {};
-  const int G = H / c.n_kv_heads, tile = c.head_dim == 128 ? 32 : 64, nsm = sms ? sms : 148;
+  const int G = H / c.n_kv_heads, nsm = sms ? sms : 148;
   const long mean = b.B ? ((long)b.rows * G + b.B - 1) / b.B : G;
   P.nt = (b.start && b.rows != b.B ? mean > 18 : 10 * ((G + 7) / 8) > 17 * ((G + 15) / 16)) ? 2 : 1;
   const int nq = 8 * P.nt;
   const long jobs = (b.start ? (long)b.rows * G / nq + b.B : (long)b.B * ((G + nq - 1) / nq)) * c.n_kv_heads;
+  const bool whole = (long)b.max_pages * c.page <= KV8_WHOLE;
+  const int tile = kv8_tile(c.head_dim, P.nt, whole);
   const long tiles = ((long)b.max_pages * c.page + tile - 1) / tile;
   P.fits = jobs * (tiles + KV8_OVER) <= 0x7fffffffL;   // units are counted in 32 bits
-  if (tiles <= KV8_WHOLE) {
+  if (whole) {
     P.blocks = (int)jobs;
-    P.warps = jobs * 2 <= nsm * kv8_resident(c.head_dim, P.nt) ? KV8_WIDE : KV8_NW;
+    P.warps = jobs <= 2 * nsm ? KV8_WIDE : KV8_NW;
     return P;
   }
-  P.blocks = (int)std::min((long)kv8_resident(c.head_dim, P.nt) * nsm, (jobs * tiles + KV8_NW - 1) / KV8_NW);
+  P.blocks = (int)std::min((long)kv8_resident(c.head_dim, P.nt, 0) * nsm, (jobs * tiles + KV8_NW - 1) / KV8_NW);
   const size_t slots = (size_t)P.blocks * KV8_NW * 2;
   P.part = slots * nq * c.head_dim;
   P.ml = slots * nq * 2;
