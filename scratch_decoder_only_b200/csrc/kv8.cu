@@ -49,8 +49,8 @@ __device__ __forceinline__ int kv8_page(const Kv8Seqs& q, const Kv8Layer& L, int
 // NaNs are the largest) and their codes, so every input byte is read once; the
 // next head's rows are loaded as soon as these are codes.  Value codes are turned over through shared
 // memory, four tokens by four channels at a time, and leave as 16 tokens of a
-// channel.  Bytes bound it for prompts, the launch for single tokens, whose
-// blocks take one head each.
+// channel.  Bytes bound it (small calls' blocks take one
+// head each).
 // ---------------------------------------------------------------------------
 struct Kv8AppendP {
   Kv8Layer L;
@@ -219,6 +219,96 @@ __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8Ap
         o[e] = make_uint4(z[0], z[1], z[2], z[3]);
       }
     }
+  }
+}
+
+// One new token per sequence (no starts), as every decode step has: a warp per
+// (sequence, head, keys | values), lanes over channels, no barrier.  Three
+// dependent loads (length, page, then the token, its page's scale and the values'
+// 16-token group together) are all there is: 2.4 us where the block form above
+// takes 4.7 (32 sequences, 12 heads of 64).
+template <typename T, int KIND, int D>
+__global__ void __launch_bounds__(128) kv8_append_one_kernel(Kv8AppendP p) {
+  griddep_wait();
+  griddep_release();
+  constexpr int E = D < 32 ? 1 : D / 32;   // channels a lane
+  const Kv8Layer& L = p.L;
+  const int lane = threadIdx.x & 31, lp = L.lp;
+  const long job = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int b = (int)(job / (2 * L.Hkv)), h = (int)(job % (2 * L.Hkv)) >> 1, c = lane * E;
+  const bool is_v = job & 1, on = D >= 32 || lane < D;
+  if (b >= p.q.B) return;
+  const int len = p.q.lens[b], slot = (len - 1) & ((1 << lp) - 1);
+  if (len < 1 || len > p.q.max_pages << lp) {
+    if (lane == 0 && h == 0) set_dev_err(p.err, GPT_DEVERR_POS);
+    return;
+  }
+  const int id = kv8_page(p.q, L, b, (len - 1) >> lp, p.err);
+  if (id < 0) return;
+  const size_t ph = (size_t)id * L.Hkv + h;
+  uint8_t* page = (is_v ? L.v : L.k) + (ph << lp) * D;
+  float* sp = (is_v ? L.vs : L.ks) + ph;
+  const uint16_t* x = (is_v ? p.v : p.k) + (long)b * (is_v ? p.ldv : p.ldk) + h * D + c;
+  uint4* group = reinterpret_cast<uint4*>(page + (slot & ~15) * D) + c;   // this lane's channels, 16 tokens each
+  unsigned raw[E], mx = 0;
+  uint4 old[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    raw[e] = on ? x[e] : 0;
+    old[e] = make_uint4(0, 0, 0, 0);
+    if (is_v && on && (slot & 15)) old[e] = group[e];
+    mx = max(mx, raw[e] & 0x7fffu);
+  }
+  const float s_old = slot > 0 ? *sp : 0.f;
+  mx = __reduce_max_sync(0xffffffffu, mx);   // (all lanes have read the scale)
+  constexpr float TOP = KIND == GPT_KV8_INT8 ? 127.f : 448.f;
+  const float a = bits16_f<T>(mx);
+  float s = a / TOP;
+  if (s < FLT_MIN) s = 0.f;             // 1 / s would overflow
+  if (s_old > s) s = s_old;
+  if (!(a <= FLT_MAX) || s_old != s_old) s = NAN;
+  const bool live = s > 0.f, recode = slot > 0 && s != s_old;
+  const float inv = live ? 1.f / s : 0.f, ratio = live ? s_old / s : 0.f;
+  if (lane == 0) *sp = s;
+  if (!is_v) {
+    if (recode) {
+      uint32_t* o = reinterpret_cast<uint32_t*>(page);
+      for (int i = lane; i < slot * (D / 4); i += 32) o[i] = live ? kv8_recode4<KIND>(o[i], ratio) : 0u;
+    }
+  } else if (recode) {
+    uint4* o = reinterpret_cast<uint4*>(page);
+    for (int i = lane; i < (slot >> 4) * D; i += 32) {
+      uint4 w = o[i];
+      w.x = live ? kv8_recode4<KIND>(w.x, ratio) : 0u;
+      w.y = live ? kv8_recode4<KIND>(w.y, ratio) : 0u;
+      w.z = live ? kv8_recode4<KIND>(w.z, ratio) : 0u;
+      w.w = live ? kv8_recode4<KIND>(w.w, ratio) : 0u;
+      o[i] = w;
+    }
+  }
+  if (!on) return;
+  float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < E; ++e) f[e] = bits16_f<T>(raw[e]) * inv;
+  const uint32_t code = live ? kv8_code4<KIND>(f[0], f[1], f[2], f[3]) : 0u;
+  if (!is_v) {
+    uint8_t* o = page + slot * D + c;
+    if constexpr (E == 4) *reinterpret_cast<uint32_t*>(o) = code;
+    else if constexpr (E == 2) *reinterpret_cast<uint16_t*>(o) = (uint16_t)code;
+    else *o = (uint8_t)code;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const uint32_t was[4] = {old[e].x, old[e].y, old[e].z, old[e].w};
+    uint32_t z[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int at = (slot & 15) - 4 * q;   // of the new byte in this word
+      const uint32_t held = recode ? (live ? kv8_recode4<KIND>(was[q], ratio) : 0u) : was[q];
+      z[q] = (held & kv8_bytes(at)) | (at >= 0 && at < 4 ? (code >> (8 * e) & 0xffu) << (8 * at) : 0u);
+    }
+    group[e] = make_uint4(z[0], z[1], z[2], z[3]);
   }
 }
 
@@ -1162,6 +1252,15 @@ static int kv8_per_block(int jobs, int n) {
 
 template <typename T, int KIND>
 static cudaError_t append_t(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 grid, cudaStream_t s) {
+  if (!p.q.start) {
+    const dim3 one((unsigned)(((long)p.q.B * c.n_kv_heads * 2 + 3) / 4));
+    switch (c.head_dim) {
+      case 16: return launch_k(kv8_append_one_kernel<T, KIND, 16>, one, dim3(128), 0, s, p);
+      case 32: return launch_k(kv8_append_one_kernel<T, KIND, 32>, one, dim3(128), 0, s, p);
+      case 64: return launch_k(kv8_append_one_kernel<T, KIND, 64>, one, dim3(128), 0, s, p);
+      default: return launch_k(kv8_append_one_kernel<T, KIND, 128>, one, dim3(128), 0, s, p);
+    }
+  }
   const size_t smem = (size_t)c.page * (c.head_dim + KV8_PAD);
   switch (c.page * c.head_dim / 1024) {
     case 0:

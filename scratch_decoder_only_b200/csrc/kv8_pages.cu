@@ -15,7 +15,6 @@
 #include <cooperative_groups.h>
 #include <algorithm>
 #include <string>
-#include <utility>
 #include "kv8.cuh"
 
 namespace cg = cooperative_groups;
@@ -106,22 +105,6 @@ __global__ void __cluster_dims__(KVP_CTAS, 1, 1) __launch_bounds__(KVP_THREADS)
   const int rank = cl.block_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P1 = (1 << p.lp) - 1, claim0 = -0x7fffffff, chunks = (p.n_pages + KVP_THREADS - 1) / KVP_THREADS;
   int *place = first + n + 1, *chunk = place + n;
-  // ---- free pages of this block's chunks, the loads ahead of everything else
-  for (int c = rank + tid * KVP_CTAS; c < chunks; c += KVP_CTAS * KVP_THREADS) chunk[c] = 0;
-  __syncthreads();
-  for (int c0 = rank; c0 < chunks; c0 += 8 * KVP_CTAS) {
-    int r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int id = (c0 + i * KVP_CTAS) * KVP_THREADS + tid;
-      r[i] = id < p.n_pages ? p.ref[id] : 1;   // (n_pages <= 2^24: no overflow)
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const unsigned m = __ballot_sync(0xffffffffu, r[i] <= 0);
-      if (lane == 0 && m) atomicAdd(&chunk[c0 + i * KVP_CTAS], __popc(m));
-    }
-  }
   if (FORK && rank == 0) {
     for (int i = tid; i < n; i += KVP_THREADS) {
       const int a = src[i], z = dst[i];
@@ -132,10 +115,7 @@ __global__ void __cluster_dims__(KVP_CTAS, 1, 1) __launch_bounds__(KVP_THREADS)
       if (first[i]) atomicMin(&p.lens[dst[i]], claim0 + i);
     __threadfence();
   }
-  cl.sync();   // counts and claims are there
-  for (int c = tid; c < chunks; c += KVP_THREADS)
-    if (c % KVP_CTAS != rank) chunk[c] = *cl.map_shared_rank(chunk + c, c % KVP_CTAS);
-  auto gathered = cl.barrier_arrive();
+  if (FORK) cl.sync();   // the claims are there
   // ---- pages that each request needs (an invalid one: none)
   int carry = 0;
   bool bad_pos = false;
@@ -173,10 +153,29 @@ __global__ void __cluster_dims__(KVP_CTAS, 1, 1) __launch_bounds__(KVP_THREADS)
   if (bad_pos && rank == 0) set_dev_err(p.err, GPT_DEVERR_POS);
   __syncthreads();
   const int total = carry;
-  cl.barrier_wait(std::move(gathered));   // the blocks have each other's counts: they may be overwritten
 
   int avail = 0x7fffffff;
-  if (total > 0) {
+  if (total > 0) {   // (as in 15 of 16 decode steps it is not)
+    // ---- free pages of this block's chunks, then of all of them
+    for (int c = rank + tid * KVP_CTAS; c < chunks; c += KVP_CTAS * KVP_THREADS) chunk[c] = 0;
+    __syncthreads();
+    for (int c0 = rank; c0 < chunks; c0 += 8 * KVP_CTAS) {
+      int r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int id = (c0 + i * KVP_CTAS) * KVP_THREADS + tid;
+        r[i] = id < p.n_pages ? p.ref[id] : 1;   // (n_pages <= 2^24: no overflow)
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const unsigned m = __ballot_sync(0xffffffffu, r[i] <= 0);
+        if (lane == 0 && m) atomicAdd(&chunk[c0 + i * KVP_CTAS], __popc(m));
+      }
+    }
+    cl.sync();   // the counts are there
+    for (int c = tid; c < chunks; c += KVP_THREADS)
+      if (c % KVP_CTAS != rank) chunk[c] = *cl.map_shared_rank(chunk + c, c % KVP_CTAS);
+    cl.sync();   // the blocks have each other's: they may be overwritten
     // ---- free pages before each chunk, and in all
     avail = 0;
     for (int c0 = 0; c0 < chunks; c0 += KVP_THREADS) {

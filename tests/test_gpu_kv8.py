@@ -166,10 +166,10 @@ def test_append_and_read(torch, kind, dtype, heads, d, page, old, new):
 
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
-def test_append_token_by_token(torch, kind):
+@pytest.mark.parametrize("P,heads,d,dtype", [(16, 2, 64, "bf16"), (32, 3, 16, "fp16"), (64, 1, 128, "bf16"), (128, 5, 32, "fp16")])
+def test_append_token_by_token(torch, kind, P, heads, d, dtype):
     """Growing values: the scale of a page rises with most tokens and its codes
     are rounded anew each time; one row per sequence, without starts."""
-    P, heads, d = 16, 2, 64
     s = Setup(torch, kind, heads, d, P, [40, 33, 8], [1, 1, 1], seed=1)
     rng = np.random.default_rng(2)
     for step in range(1, 34):
@@ -177,8 +177,8 @@ def test_append_token_by_token(torch, kind):
         live = [i for i, n in enumerate(lens) if n]
         from scratch_decoder_only_b200.kv8 import KV8Batch
         b = KV8Batch(i32(torch, s.table[live]), i32(torch, [lens[i] for i in live]))
-        k, kf = values(torch, rng, (len(live), heads, d), "bf16", 0.1 * step)
-        v, vf = values(torch, rng, (len(live), heads, d), "bf16", 4.0 / step)
+        k, kf = values(torch, rng, (len(live), heads, d), dtype, 0.1 * step)
+        v, vf = values(torch, rng, (len(live), heads, d), dtype, 4.0 / step)
         s.cache.append(0, k.cuda(), v.cuda(), b)
         for j, i in enumerate(live):
             s.ref.append(s.table[i], lens[i], (kf[j:j + 1], vf[j:j + 1]))
