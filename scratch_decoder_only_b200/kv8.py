@@ -171,6 +171,8 @@ class KV8Cache(_Calls):
 
     def batch(self, start=None, rows=None) -> KV8Batch:
         """All rows of the cache's own table."""
+        if self.table is None or self.lens is None:
+            raise ValueError("this cache was made without table and lens")
         return KV8Batch(self.table, self.lens, start, rows)
 
     # -- plumbing
@@ -209,6 +211,8 @@ class KV8Cache(_Calls):
         """(k, v) [rows, heads, head_dim]: what the cache holds of the batch's
         tokens.  Rows without a token in the cache are not written."""
         b = self._batch(batch)
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be bfloat16 or float16")
         h, d = self.n_kv_heads, self.head_dim
         ld = h * d
         k = _new((b.rows, h, d), (ld, d, 1), dtype=dtype, device=self.device)
@@ -222,6 +226,8 @@ class KV8Cache(_Calls):
         natural log of the softmax denominators [rows, n_heads]."""
         b = self._batch(batch)
         d, dev = self.head_dim, self.device
+        if q.dim() not in (2, 3):
+            raise ValueError("q must be [rows, n_heads, head_dim] or [rows, n_heads * head_dim]")
         H = q.shape[1] if q.dim() == 3 else q.shape[1] // d
         pq, ldq = self._rows(q, "q", b.rows, H)
         if out is None:

@@ -236,6 +236,7 @@ ATTENDS = [
     (3, 2, 16, 32, [700], [17]),
     (1, 12, 64, 16, [50, 51], [1, 1]),
     (1, 40, 32, 16, [20, 400], [1, 1]),
+    (1, 16, 128, 64, [300, 40], [1, 1]),
 ]
 
 
@@ -335,6 +336,18 @@ def test_many_sequences(torch, top, ragged):
     k, v = s.cache.read(0, s.batch(torch, True, new=lens), torch.float16)
     want = np.concatenate([s.ref.tokens(1, s.table[i], lens[i]) for i in range(B)])
     assert np.all(np.abs(v.double().cpu().numpy() - want) <= np.abs(want) * (2.0 ** -11 + 2.0 ** -23) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("G,d", [(1, 128), (12, 64), (16, 128), (2, 16)])
+def test_many_short_jobs(torch, G, d):
+    """More whole jobs than blocks of eight warps fit at once: blocks of four."""
+    rng = np.random.default_rng(d)
+    B = 160
+    lens, new = [int(n) for n in rng.integers(0, 120, B)], [1] * B
+    s = Setup(torch, "e4m3", 2, d, 32, lens, new, seed=d)
+    q, qf = values(torch, s.rng, (B, 2 * G, d), "bf16")
+    out, lse = s.cache.attention(0, q.cuda(), s.batch(torch, False), return_lse=True)
+    check(torch, s, qf, out, lse, lens, new, "bf16")
 
 
 def test_attention_of_equal_weights(torch):
@@ -635,6 +648,58 @@ def test_pages_of_a_large_pool(torch):
     c.extend(i32(torch, add))
     assert p.extend(add) == c.status() != 0
     same_pool(c, p)
+
+
+def test_pages_of_the_most_rows(torch):
+    """16384 rows: as much shared memory as a call can ask for."""
+    from scratch_decoder_only_b200.kv8 import KV8Cache
+    rng = np.random.default_rng(6)
+    rows, pages = 16384, 40009
+    c = KV8Cache.empty(1, pages, 1, 16, page=16, n_rows=rows, max_pages=5)
+    p = R.Pool(rows, 5, pages, 16)
+    for _ in range(2):
+        add = rng.integers(0, 40, size=rows)
+        c.extend(i32(torch, add))
+        assert p.extend(add) == c.status()
+        same_pool(c, p)
+        out = np.unique(rng.integers(0, rows, size=rows))
+        c.free(i32(torch, out))
+        p.free(out)
+    empty = np.nonzero(p.lens == 0)[0]
+    src = rng.integers(0, rows, size=len(empty))
+    got = c.fork(i32(torch, src), i32(torch, empty))
+    done, _, bits = p.fork(src, empty)
+    assert np.array_equal(got.cpu().numpy(), done) and c.status() == bits
+    same_pool(c, p)
+
+
+def test_python_refusals(torch):
+    """What the binding refuses before a call."""
+    from scratch_decoder_only_b200.kv8 import KV8Batch, KV8Cache, KV8Pool
+    c = KV8Cache.empty(1, 8, 2, 64, n_rows=3, max_pages=4)
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    b = c.batch()
+    bad = [lambda: c.append(0, x.float(), x.float()), lambda: c.append(0, x, x.half()), lambda: c.append(0, x[:2], x[:2]),
+           lambda: c.append(0, x.cpu(), x), lambda: c.append(0, x.transpose(0, 1).contiguous().transpose(0, 1), x),
+           lambda: c.append(0, x[:, :, ::2], x), lambda: c.attention(0, x[0, 0], b), lambda: c.attention(0, x, b, out=x[:1]),
+           lambda: c.attention(0, x, b, out=torch.zeros_like(x).half()), lambda: c.read(0, b, torch.float32),
+           lambda: KV8Batch(c.table, c.lens[:2]), lambda: KV8Batch(c.table, c.lens, c.lens), lambda: KV8Batch(c.table.long(), c.lens),
+           lambda: KV8Batch(c.table, c.lens, rows=4), lambda: KV8Batch(c.table.cpu(), c.lens),
+           lambda: KV8Cache(c.k, c.v[:, :4], c.k_scale, c.v_scale), lambda: KV8Cache(c.k.cpu(), c.v.cpu(), c.k_scale, c.v_scale),
+           lambda: KV8Cache(c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale, c.v_scale),
+           lambda: KV8Cache(c.k, c.v, c.k_scale.half(), c.v_scale), lambda: KV8Cache(c.k, c.v, c.k_scale, c.v_scale).batch(),
+           lambda: KV8Cache(c.k, c.v, c.k_scale, c.v_scale).compact(), lambda: KV8Cache(c.k, c.v, c.k_scale, c.v_scale, c.table, c.lens, c.ref[:4]),
+           lambda: c.extend(c.lens[:2]), lambda: c.extend(c.lens.long()), lambda: c.fork(c.lens, c.lens[:1]), lambda: c.free(c.lens.cpu()),
+           lambda: KV8Pool(c.table, c.lens[:1], c.ref, 16)]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    from scratch_decoder_only_b200.gpt import GPTError
+    for f in (lambda: c.append(1, x, x), lambda: c.attention(0, torch.zeros(3, 3, 64, dtype=torch.bfloat16, device="cuda"), b),
+              lambda: c.attention(0, x, b, scale=float("nan"))):
+        with pytest.raises(GPTError):
+            f()
+    assert c.status() == 0 and not c.k.view(torch.uint8).any()
 
 
 def test_free_of_pages_nobody_holds(torch):
