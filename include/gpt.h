@@ -520,7 +520,7 @@ int gpt_kv8_attention_work(const gpt_kv8_cache* c, const gpt_kv8_batch* b, int n
 
 /* Which pages the rows (sequences) of a cache hold, kept on the device.
  *  table  device int32 [n_rows][ld_table]: entries 0 .. ceil(lens/page) - 1 of
- *         a row are its pages; the others are never read, and -1 once freed
+ *         a row are its pages; the others are never used, and -1 once freed
  *  lens   device int32 [n_rows]: tokens of each row (0: empty)
  *  ref    device int32 [n_pages]: rows that hold the page (0: free)
  * All zero lens and refs is an empty pool.  n_rows <= 16384, n_pages <= 2^24. */

@@ -630,13 +630,26 @@ struct Kv8Tile {
 };
 template <int D, int NT, int NW>
 constexpr size_t kv8_attn_smem() {
-  return (size_t)(NW ? NW : KV8_NW) * 2 * Kv8Tile<D, NT, NW != 0>::HALF + (size_t)(NW / 2) * 8 * NT * (D + 4) * 4;
+  return (size_t)(NW ? NW : KV8_NW) * 2 * Kv8Tile<D, NT, NW != 0>::HALF + (size_t)NW * 8 * NT * (D + 4) * 4;
 }
 // Blocks an SM holds by their registers: of four warps 128, 168 or 255 a thread, of
 // eight 128 (255 where 16 queries of 128 channels need them).
 __host__ __device__ constexpr int kv8_resident(int D, int nt, int nw) {
   return nw == KV8_WIDE ? (nt == 2 && D == 128 ? 1 : 2)
                         : nt == 1 && (D < 128 || nw) ? 4 : nt == 1 || D < 128 ? 3 : 2;
+}
+
+// Two partial results of a query, four channels.
+struct Kv8Sum {
+  float M, l;
+  float4 y;
+};
+__device__ __forceinline__ void kv8_join(Kv8Sum& a, float M, float l, float4 y) {
+  const float Mn = fmaxf(a.M, M), mu = Mn == -INFINITY ? 0.f : Mn, f = kv8_ex2(a.M - mu), g = kv8_ex2(M - mu);
+  a.M = Mn;
+  a.l = a.l * f + l * g;
+  a.y.x = a.y.x * f + y.x * g; a.y.y = a.y.y * f + y.y * g;
+  a.y.z = a.y.z * f + y.z * g; a.y.w = a.y.w * f + y.w * g;
 }
 
 // The result of query q0 + n of a job, four channels from d on.
@@ -678,6 +691,8 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
   if (!WHOLE && lane < 2) p.piece[2 * run + lane].pieces = 0;
   if (!kv8_locate<NQ, TILE, WHOLE>(p, gridDim.x * KV8_NW, blockIdx.x * (WHOLE ? 1 : KV8_NW), r)) return;
   if (!WHOLE && (r.u >= r.total || r.b < 0)) return;   // no barrier follows
+  // a whole job's first page ids do not wait for its length
+  const uint32_t id0 = WHOLE ? p.q.table[(long)r.b * p.q.ld_table + min((warp * TILE + TQ * t) >> lp, p.q.max_pages - 1)] : 0;
   Kv8Share sh = kv8_share<NQ, TILE>(p, r.b);
   // units of this run, counted from its begin; a job's first KV8_OVER have no tile
   const int R = WHOLE ? sh.tiles : min(r.quota, r.total - r.u);
@@ -692,11 +707,11 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
     nu = -nt;
     nt = 0;
   }
-  auto page = [&]() {
+  auto page = [&](bool first) {
     const int tok = nt * TILE + TQ * t;
     nph = KV8_NONE;
     if (nu < R && tok < nlen) {
-      const uint32_t id = p.q.table[(long)nb * p.q.ld_table + (tok >> lp)];
+      const uint32_t id = first ? id0 : p.q.table[(long)nb * p.q.ld_table + (tok >> lp)];
       if (id < (uint32_t)L.n_pages) nph = id * Hkv + nh;
       else set_dev_err(p.err, GPT_DEVERR_PAGE);
     }
@@ -725,7 +740,7 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
         }
       }
     }
-    page();
+    page(false);
   };
   const uint32_t kbuf = (uint32_t)__cvta_generic_to_shared(ring) + warp * 2 * HALF, vbuf = kbuf + HALF;
   float ks_next = 0.f, vs_next = 0.f;
@@ -768,7 +783,7 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
     nu += warp;
     nt += warp;
   }
-  page();
+  page(WHOLE);
   fetch_keys();
   advance();
 
@@ -1010,57 +1025,34 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
         }
       }
     if constexpr (WHOLE) {
-      // ---- merge the warps, the upper half into the lower one each time; warp 0's result goes out
+      // ---- merge the warps' queries, each warp's in a buffer of its own
       constexpr int ROW = D + 4;
-      float* so = reinterpret_cast<float*>(ring + WARPS * 2 * HALF);   // [WARPS / 2][NQ][ROW]
-      __shared__ float sm[WARPS / 2][NQ], sl[WARPS / 2][NQ];
-      auto put = [&](int at) {
+      float* so = reinterpret_cast<float*>(ring + WARPS * 2 * HALF);   // [WARPS][NQ][ROW]
+      __shared__ float sm[WARPS][NQ], sl[WARPS][NQ];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int n = j * 8 + 2 * t + e;
+        for (int e = 0; e < 2; ++e) {
+          const int n = j * 8 + 2 * t + e;
+          if (n >= nq) continue;
 #pragma unroll
-            for (int i = 0; i < KW; ++i) {
-              so[(at * NQ + n) * ROW + i * 16 + c] = o[j][i][e];
-              so[(at * NQ + n) * ROW + i * 16 + c + 8] = o[j][i][e + 2];
-            }
-            if (c == 0) {
-              sm[at][n] = m[j][e];
-              sl[at][n] = l[j][e];
-            }
+          for (int i = 0; i < KW; ++i) {
+            so[(warp * NQ + n) * ROW + i * 16 + c] = o[j][i][e];
+            so[(warp * NQ + n) * ROW + i * 16 + c + 8] = o[j][i][e + 2];
           }
-      };
-      auto take = [&](int at) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int n = j * 8 + 2 * t + e;
-            const float m2 = sm[at][n], M = fmaxf(m[j][e], m2), mu = M == -INFINITY ? 0.f : M;
-            const float f1 = kv8_ex2(m[j][e] - mu), f2 = kv8_ex2(m2 - mu);
-            m[j][e] = M;
-            l[j][e] = l[j][e] * f1 + sl[at][n] * f2;
-#pragma unroll
-            for (int i = 0; i < KW; ++i) {
-              o[j][i][e] = o[j][i][e] * f1 + so[(at * NQ + n) * ROW + i * 16 + c] * f2;
-              o[j][i][e + 2] = o[j][i][e + 2] * f1 + so[(at * NQ + n) * ROW + i * 16 + c + 8] * f2;
-            }
+          if (c == 0) {
+            sm[warp][n] = m[j][e];
+            sl[warp][n] = l[j][e];
           }
-      };
-#pragma unroll
-      for (int half = WARPS / 2; half; half >>= 1) {
-        if (sh.tiles <= half) continue;   // those warps had no tile
-        if (warp >= half && warp < 2 * half) put(warp - half);
-        __syncthreads();
-        if (warp < half) take(warp);
-        __syncthreads();
-      }
-      if (warp == 0) put(0);
+        }
       __syncthreads();
+      const int used = min(WARPS, sh.tiles);   // warps that had a tile
       for (int i = threadIdx.x; i < nq * (D / 4); i += 32 * WARPS) {
         const int n = i / (D / 4), d = (i % (D / 4)) * 4;
-        kv8_out<T>(p, sh.s0, h, q0 + n, d, D, *reinterpret_cast<const float4*>(so + n * ROW + d), sm[0][n], sl[0][n]);
+        Kv8Sum a = {sm[0][n], sl[0][n], *reinterpret_cast<const float4*>(so + n * ROW + d)};
+        for (int w = 1; w < used; ++w)
+          kv8_join(a, sm[w][n], sl[w][n], *reinterpret_cast<const float4*>(so + (w * NQ + n) * ROW + d));
+        kv8_out<T>(p, sh.s0, h, q0 + n, d, D, a.y, a.M, a.l);
       }
       return;
     } else {
@@ -1123,18 +1115,6 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
 // query) over all pieces: threads over columns, and over pieces where the share
 // has fewer columns than threads.  Latency bounds it: a look at what the run left,
 // then loads that do not depend on one another.
-struct Kv8Sum {
-  float M, l;
-  float4 y;
-};
-__device__ __forceinline__ void kv8_join(Kv8Sum& a, float M, float l, float4 y) {
-  const float Mn = fmaxf(a.M, M), mu = Mn == -INFINITY ? 0.f : Mn, f = kv8_ex2(a.M - mu), g = kv8_ex2(M - mu);
-  a.M = Mn;
-  a.l = a.l * f + l * g;
-  a.y.x = a.y.x * f + y.x * g; a.y.y = a.y.y * f + y.y * g;
-  a.y.z = a.y.z * f + y.z * g; a.y.w = a.y.w * f + y.w * g;
-}
-
 // A column of job J over the pieces first, first + step, ...
 template <int NQ, int D>
 __device__ __forceinline__ Kv8Sum kv8_gather(const Kv8AttnP& p, const Kv8Piece& J, int col, int first, int step) {
