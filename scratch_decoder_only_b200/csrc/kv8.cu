@@ -7,6 +7,18 @@
 #include <type_traits>
 #include "kv8.cuh"
 
+__device__ __forceinline__ void kv8_copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void kv8_lds(uint32_t* r, uint32_t src) {
+  if constexpr (N == 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(src) : "memory");
+  else if constexpr (N == 8) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(src) : "memory");
+  else
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(src) : "memory");
+}
+
 // The part of a sequence that an append or read job covers: unit `unit` of
 // 1 << lu tokens (a page, or 16 tokens), slots [lo, hi) of it, the row of the
 // call's matrices that holds slot lo.  All threads of the block call this.
@@ -43,11 +55,11 @@ __device__ __forceinline__ int kv8_page(const Kv8Seqs& q, const Kv8Layer& L, int
 
 // ---------------------------------------------------------------------------
 // Append.  A block of 128 threads takes a page of a sequence and a run of heads,
-// keys or values, one head after the other.  A head's new rows stay in registers
-// (VPT 16-byte vectors a thread) between their largest magnitude (an unsigned
+// keys or values, one head after the other.  The next head's rows travel by
+// asynchronous copies into shared memory, each thread's to places of its own, while
+// a head's stay in registers (VPT 16-byte vectors a thread) between their largest magnitude (an unsigned
 // 16-bit maximum over the bit patterns without the sign, in which infinities and
-// NaNs are the largest) and their codes, so every input byte is read once; the
-// next head's rows are loaded as soon as these are codes.  Value codes are turned over through shared
+// NaNs are the largest) and their codes, so every input byte is read once.  Value codes are turned over through shared
 // memory, four tokens by four channels at a time, and leave as 16 tokens of a
 // channel.  Bytes bound it (small calls' blocks take one
 // head each).
@@ -115,7 +127,9 @@ template <typename T, int KIND, int VPT>
 __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8AppendP p) {
   griddep_wait();
   griddep_release();
-  extern __shared__ __align__(16) uint8_t turn[];   // value codes [P][D + KV8_PAD]
+  // the next head's rows, [VPT][128] vectors, each thread's own; value codes [P][D + KV8_PAD]
+  extern __shared__ __align__(16) uint8_t ahead[];
+  uint8_t* turn = ahead + VPT * 128 * 16;
   __shared__ unsigned wmax[2][4];
   const Kv8Layer& L = p.L;
   const int tid = threadIdx.x, lp = L.lp, ld = L.ld, D = 1 << ld;
@@ -133,23 +147,32 @@ __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8Ap
   const int mine = (nv - tid + 127) >> 7;   // vectors of this thread
   const long step = (128L >> (ld - 3)) * ldx;
   x += (long)(tid >> (ld - 3)) * ldx + ((tid & ((D >> 3) - 1)) << 3);
-  uint4 r[VPT];
-  float s_old = 0.f;
+  const uint32_t slot = (uint32_t)__cvta_generic_to_shared(ahead) + tid * 16;
+  float s_next = 0.f;
   auto load = [&](int h) {
     const uint16_t* y = x + (h << ld);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j, y += step) r[j] = j < mine ? *reinterpret_cast<const uint4*>(y) : make_uint4(0, 0, 0, 0);
-    s_old = u.lo > 0 ? scales[h] : 0.f;   // read by all before the barrier, written behind it
+    for (int j = 0; j < VPT; ++j, y += step)
+      if (j < mine) kv8_copy16(slot + j * 128 * 16, reinterpret_cast<const uint8_t*>(y));
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    s_next = u.lo > 0 ? scales[h] : 0.f;   // read by all before the barrier, written behind it
   };
   load(h0);
   for (int h = h0; h < h1; ++h) {
-    unsigned mx = 0;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    uint4 r[VPT];
+    unsigned pair = 0;   // the largest magnitudes of even and odd elements
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const unsigned a = __vmaxu2(__vmaxu2(r[j].x & 0x7fff7fffu, r[j].y & 0x7fff7fffu),
-                                  __vmaxu2(r[j].z & 0x7fff7fffu, r[j].w & 0x7fff7fffu));
-      mx = max(mx, max(a & 0xffffu, a >> 16));
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (j < mine) kv8_lds<16>(w, slot + j * 128 * 16);
+      r[j] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pair = __vmaxu2(pair, w[e] & 0x7fff7fffu);
     }
+    const float s_old = s_next;
+    if (h + 1 < h1) load(h + 1);
+    unsigned mx = max(pair & 0xffffu, pair >> 16);
     mx = __reduce_max_sync(0xffffffffu, mx);
     if ((tid & 31) == 0) wmax[h & 1][tid >> 5] = mx;
     __syncthreads();   // (also: the turning buffer's codes of the head before have been read)
@@ -184,7 +207,6 @@ __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8Ap
           *reinterpret_cast<uint2*>(o + j * (128 >> (ld - 3)) * row) =
               live ? kv8_code8<T, KIND>(r[j], inv) : make_uint2(0, 0);
     }
-    if (h + 1 < h1) load(h + 1);
     if (!is_v) continue;
     __syncthreads();
     // 16-token groups that change: those with new tokens, all earlier ones too when the scale grew; a thread
@@ -488,17 +510,6 @@ __device__ __forceinline__ uint32_t kv8_transpose8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-__device__ __forceinline__ void kv8_copy16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void kv8_lds(uint32_t* r, uint32_t src) {
-  if constexpr (N == 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(src) : "memory");
-  else if constexpr (N == 8) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(src) : "memory");
-  else
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(src) : "memory");
 }
 // keep the low n bytes of four
 __device__ __forceinline__ uint32_t kv8_low_bytes(uint32_t w, int n) {
@@ -1247,6 +1258,16 @@ static int kv8_per_block(int jobs, int n) {
   return (n + groups - 1) / groups;
 }
 
+template <typename T, int KIND, int VPT>
+static cudaError_t append_v(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 grid, cudaStream_t s) {
+  const size_t smem = (size_t)VPT * 128 * 16 + (size_t)c.page * (c.head_dim + KV8_PAD);
+  if (VPT == 16) {   // 50 KB
+    const cudaError_t e = cudaFuncSetAttribute(kv8_append_kernel<T, KIND, VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 56 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_k(kv8_append_kernel<T, KIND, VPT>, grid, dim3(128), smem, s, p);
+}
+
 template <typename T, int KIND>
 static cudaError_t append_t(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 grid, cudaStream_t s) {
   if (!p.q.start) {
@@ -1258,14 +1279,13 @@ static cudaError_t append_t(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 gr
       default: return launch_k(kv8_append_one_kernel<T, KIND, 128>, one, dim3(128), 0, s, p);
     }
   }
-  const size_t smem = (size_t)c.page * (c.head_dim + KV8_PAD);
   switch (c.page * c.head_dim / 1024) {
     case 0:
-    case 1: return launch_k(kv8_append_kernel<T, KIND, 1>, grid, dim3(128), smem, s, p);
-    case 2: return launch_k(kv8_append_kernel<T, KIND, 2>, grid, dim3(128), smem, s, p);
-    case 4: return launch_k(kv8_append_kernel<T, KIND, 4>, grid, dim3(128), smem, s, p);
-    case 8: return launch_k(kv8_append_kernel<T, KIND, 8>, grid, dim3(128), smem, s, p);
-    default: return launch_k(kv8_append_kernel<T, KIND, 16>, grid, dim3(128), smem, s, p);
+    case 1: return append_v<T, KIND, 1>(p, c, grid, s);
+    case 2: return append_v<T, KIND, 2>(p, c, grid, s);
+    case 4: return append_v<T, KIND, 4>(p, c, grid, s);
+    case 8: return append_v<T, KIND, 8>(p, c, grid, s);
+    default: return append_v<T, KIND, 16>(p, c, grid, s);
   }
 }
 
