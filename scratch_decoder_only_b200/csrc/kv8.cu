@@ -55,14 +55,18 @@ __device__ __forceinline__ int kv8_page(const Kv8Seqs& q, const Kv8Layer& L, int
 
 // ---------------------------------------------------------------------------
 // Append.  A block of 128 threads takes a page of a sequence and a run of heads,
-// keys or values, one head after the other.  The next head's rows travel by
-// asynchronous copies into shared memory, each thread's to places of its own, while
-// a head's stay in registers (VPT 16-byte vectors a thread) between their largest magnitude (an unsigned
-// 16-bit maximum over the bit patterns without the sign, in which infinities and
-// NaNs are the largest) and their codes, so every input byte is read once.  Value codes are turned over through shared
-// memory, four tokens by four channels at a time, and leave as 16 tokens of a
-// channel.  Bytes bound it (small calls' blocks take one
-// head each).
+// keys or values, one head after the other, or four at a time, a warp each, where a
+// page has at most 2048 elements of a head (TPH threads a head).  The next head's
+// rows travel by asynchronous copies into shared memory, each thread's to places
+// of its own, while a head's stay in registers (VPT 16-byte vectors a thread)
+// between their largest magnitude (an unsigned 16-bit maximum over the bit
+// patterns without the sign, in which infinities and NaNs are the largest) and
+// their codes, so every input byte is read once.  Value codes are turned over
+// through shared memory, four tokens by four channels at a time, and leave as 16
+// tokens of a channel.  Instruction issue bounds it, not far above the bytes: 29181
+// tokens of 64 ragged prompts, 8 heads of 128, pages of 64: 39 us (27 at the copy
+// rate); 16 x 1024 tokens, 12 heads of 64, pages of 16: 25 us (11.5; 40 with a
+// block per head instead of a warp).
 // ---------------------------------------------------------------------------
 struct Kv8AppendP {
   Kv8Layer L;
@@ -123,16 +127,21 @@ __device__ __forceinline__ void kv8_turn4(uint32_t* w) {
 
 // (the second bound: 96 registers a thread up to 8 vectors, so that enough blocks are resident to cover a block's chain
 // of dependent loads)
-template <typename T, int KIND, int VPT>
+template <typename T, int KIND, int VPT, int TPH>
 __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8AppendP p) {
   griddep_wait();
   griddep_release();
   // the next head's rows, [VPT][128] vectors, each thread's own; value codes [P][D + KV8_PAD]
   extern __shared__ __align__(16) uint8_t ahead[];
-  uint8_t* turn = ahead + VPT * 128 * 16;
   __shared__ unsigned wmax[2][4];
+  constexpr int HEADS = 128 / TPH;   // at a time
   const Kv8Layer& L = p.L;
-  const int tid = threadIdx.x, lp = L.lp, ld = L.ld, D = 1 << ld;
+  const int tid = threadIdx.x % TPH, mate = threadIdx.x / TPH, lp = L.lp, ld = L.ld, D = 1 << ld, row = D + KV8_PAD;
+  uint8_t* turn = ahead + VPT * 128 * 16 + mate * (row << lp);
+  auto meet = [] {
+    if constexpr (TPH == 128) __syncthreads();
+    else __syncwarp();
+  };
   const int h0 = blockIdx.y * p.heads, h1 = min(h0 + p.heads, L.Hkv);
   const bool is_v = blockIdx.z != 0;
   Kv8Unit u;
@@ -143,11 +152,11 @@ __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8Ap
   const uint16_t* x = (is_v ? p.v : p.k) + (long)u.row * ldx;
   float* scales = (is_v ? L.vs : L.ks) + (size_t)id * L.Hkv;
   const int nv = (u.hi - u.lo) << (ld - 3);
-  // vector tid + 128 j of a head: this thread's first one, and 128 vectors further
-  const int mine = (nv - tid + 127) >> 7;   // vectors of this thread
-  const long step = (128L >> (ld - 3)) * ldx;
+  // vector tid + TPH j of a head: this thread's first one, and TPH vectors further
+  const int mine = (nv - tid + TPH - 1) / TPH;   // vectors of this thread
+  const long step = (long)(TPH >> (ld - 3)) * ldx;
   x += (long)(tid >> (ld - 3)) * ldx + ((tid & ((D >> 3) - 1)) << 3);
-  const uint32_t slot = (uint32_t)__cvta_generic_to_shared(ahead) + tid * 16;
+  const uint32_t slot = (uint32_t)__cvta_generic_to_shared(ahead) + threadIdx.x * 16;
   float s_next = 0.f;
   auto load = [&](int h) {
     const uint16_t* y = x + (h << ld);
@@ -157,8 +166,8 @@ __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8Ap
     asm volatile("cp.async.commit_group;" ::: "memory");
     s_next = u.lo > 0 ? scales[h] : 0.f;   // read by all before the barrier, written behind it
   };
-  load(h0);
-  for (int h = h0; h < h1; ++h) {
+  if (h0 + mate < h1) load(h0 + mate);
+  for (int h = h0 + mate, par = 0; h < h1; h += HEADS, par ^= 1) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     uint4 r[VPT];
     unsigned pair = 0;   // the largest magnitudes of even and odd elements
@@ -171,12 +180,12 @@ __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8Ap
       for (int e = 0; e < 4; ++e) pair = __vmaxu2(pair, w[e] & 0x7fff7fffu);
     }
     const float s_old = s_next;
-    if (h + 1 < h1) load(h + 1);
+    if (h + HEADS < h1) load(h + HEADS);
     unsigned mx = max(pair & 0xffffu, pair >> 16);
     mx = __reduce_max_sync(0xffffffffu, mx);
-    if ((tid & 31) == 0) wmax[h & 1][tid >> 5] = mx;
-    __syncthreads();   // (also: the turning buffer's codes of the head before have been read)
-    mx = max(max(wmax[h & 1][0], wmax[h & 1][1]), max(wmax[h & 1][2], wmax[h & 1][3]));
+    if (TPH == 128 && (tid & 31) == 0) wmax[par][tid >> 5] = mx;
+    meet();   // (also: the turning buffer's codes of the head before have been read)
+    if (TPH == 128) mx = max(max(wmax[par][0], wmax[par][1]), max(wmax[par][2], wmax[par][3]));
     constexpr float TOP = KIND == GPT_KV8_INT8 ? 127.f : 448.f;
     const float a = bits16_f<T>(mx);
     float s = a / TOP;
@@ -189,30 +198,29 @@ __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8Ap
     const float ratio = live ? s_old / s : 0.f;
     if (tid == 0) scales[h] = s;
     uint8_t* page = (is_v ? L.v : L.k) + (((size_t)id * L.Hkv + h) << (lp + ld));
-    const int row = D + KV8_PAD;
     if (!is_v) {
       if (recode) {
         uint32_t* o = reinterpret_cast<uint32_t*>(page);
-        for (int i = tid; i < (u.lo << (ld - 2)); i += 128) o[i] = live ? kv8_recode4<KIND>(o[i], ratio) : 0u;
+        for (int i = tid; i < (u.lo << (ld - 2)); i += TPH) o[i] = live ? kv8_recode4<KIND>(o[i], ratio) : 0u;
       }
       uint2* o = reinterpret_cast<uint2*>(page + (u.lo << ld)) + tid;
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
-        if (j < mine) o[128 * j] = live ? kv8_code8<T, KIND>(r[j], inv) : make_uint2(0, 0);
+        if (j < mine) o[TPH * j] = live ? kv8_code8<T, KIND>(r[j], inv) : make_uint2(0, 0);
     } else {
       uint8_t* o = turn + (u.lo + (tid >> (ld - 3))) * row + ((tid & ((D >> 3) - 1)) << 3);
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
         if (j < mine)
-          *reinterpret_cast<uint2*>(o + j * (128 >> (ld - 3)) * row) =
+          *reinterpret_cast<uint2*>(o + j * (TPH >> (ld - 3)) * row) =
               live ? kv8_code8<T, KIND>(r[j], inv) : make_uint2(0, 0);
     }
     if (!is_v) continue;
-    __syncthreads();
+    meet();
     // 16-token groups that change: those with new tokens, all earlier ones too when the scale grew; a thread
     // takes four channels of one
     const int g0 = recode ? 0 : u.lo >> 4, g1 = (u.hi + 15) >> 4;
-    for (int i = (g0 << (ld - 2)) + tid; i < (g1 << (ld - 2)); i += 128) {
+    for (int i = (g0 << (ld - 2)) + tid; i < (g1 << (ld - 2)); i += TPH) {
       const int t0 = (i >> (ld - 2)) << 4, d = (i << 2) & (D - 1);
       uint32_t w[4][4];   // [four tokens][channel]
 #pragma unroll
@@ -1258,18 +1266,21 @@ static int kv8_per_block(int jobs, int n) {
   return (n + groups - 1) / groups;
 }
 
-template <typename T, int KIND, int VPT>
-static cudaError_t append_v(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 grid, cudaStream_t s) {
-  const size_t smem = (size_t)VPT * 128 * 16 + (size_t)c.page * (c.head_dim + KV8_PAD);
+template <typename T, int KIND, int VPT, int TPH>
+static cudaError_t append_v(Kv8AppendP p, const gpt_kv8_cache& c, int jobs, cudaStream_t s) {
+  const size_t smem = (size_t)VPT * 128 * 16 + (size_t)(128 / TPH) * c.page * (c.head_dim + KV8_PAD);
   if (VPT == 16) {   // 50 KB
-    const cudaError_t e = cudaFuncSetAttribute(kv8_append_kernel<T, KIND, VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 56 * 1024);
+    const cudaError_t e = cudaFuncSetAttribute(kv8_append_kernel<T, KIND, VPT, TPH>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 56 * 1024);
     if (e != cudaSuccess) return e;
   }
-  return launch_k(kv8_append_kernel<T, KIND, VPT>, grid, dim3(128), smem, s, p);
+  p.heads = kv8_per_block(jobs, (c.n_kv_heads * TPH + 127) / 128) * (128 / TPH);
+  const dim3 grid(jobs, (c.n_kv_heads + p.heads - 1) / p.heads, 2);
+  return launch_k(kv8_append_kernel<T, KIND, VPT, TPH>, grid, dim3(128), smem, s, p);
 }
 
 template <typename T, int KIND>
-static cudaError_t append_t(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 grid, cudaStream_t s) {
+static cudaError_t append_t(const Kv8AppendP& p, const gpt_kv8_cache& c, int jobs, cudaStream_t s) {
   if (!p.q.start) {
     const dim3 one((unsigned)(((long)p.q.B * c.n_kv_heads * 2 + 3) / 4));
     switch (c.head_dim) {
@@ -1279,13 +1290,14 @@ static cudaError_t append_t(const Kv8AppendP& p, const gpt_kv8_cache& c, dim3 gr
       default: return launch_k(kv8_append_one_kernel<T, KIND, 128>, one, dim3(128), 0, s, p);
     }
   }
-  switch (c.page * c.head_dim / 1024) {
-    case 0:
-    case 1: return append_v<T, KIND, 1>(p, c, grid, s);
-    case 2: return append_v<T, KIND, 2>(p, c, grid, s);
-    case 4: return append_v<T, KIND, 4>(p, c, grid, s);
-    case 8: return append_v<T, KIND, 8>(p, c, grid, s);
-    default: return append_v<T, KIND, 16>(p, c, grid, s);
+  switch (c.page * c.head_dim) {
+    case 256: return append_v<T, KIND, 1, 32>(p, c, jobs, s);
+    case 512: return append_v<T, KIND, 2, 32>(p, c, jobs, s);
+    case 1024: return append_v<T, KIND, 4, 32>(p, c, jobs, s);
+    case 2048: return append_v<T, KIND, 8, 32>(p, c, jobs, s);
+    case 4096: return append_v<T, KIND, 4, 128>(p, c, jobs, s);
+    case 8192: return append_v<T, KIND, 8, 128>(p, c, jobs, s);
+    default: return append_v<T, KIND, 16, 128>(p, c, jobs, s);
   }
 }
 
@@ -1389,15 +1401,13 @@ int gpt_kv8_append(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, co
   if (b->B == 0 || b->rows == 0) return GPT_OK;
   Kv8AppendP p = {kv8_layer(*c, layer), kv8_seqs(*b), (const uint16_t*)k, (const uint16_t*)v, ldk, ldv, 0, err};
   const int jobs = kv8_jobs(*b, p.L.lp);
-  p.heads = kv8_per_block(jobs, c->n_kv_heads);
-  const dim3 grid(jobs, (c->n_kv_heads + p.heads - 1) / p.heads, 2);
   cudaStream_t s = (cudaStream_t)stream;
   const bool i8 = c->kind == GPT_KV8_INT8;
   ++g_kernel_launches;
   return kv8_done("gpt_kv8_append",
                   dtype == GPT_PRECISION_BF16
-                      ? (i8 ? append_t<bf16, GPT_KV8_INT8>(p, *c, grid, s) : append_t<bf16, GPT_KV8_E4M3>(p, *c, grid, s))
-                      : (i8 ? append_t<f16, GPT_KV8_INT8>(p, *c, grid, s) : append_t<f16, GPT_KV8_E4M3>(p, *c, grid, s)));
+                      ? (i8 ? append_t<bf16, GPT_KV8_INT8>(p, *c, jobs, s) : append_t<bf16, GPT_KV8_E4M3>(p, *c, jobs, s))
+                      : (i8 ? append_t<f16, GPT_KV8_INT8>(p, *c, jobs, s) : append_t<f16, GPT_KV8_E4M3>(p, *c, jobs, s)));
 }
 
 int gpt_kv8_read(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, void* k, long ldk, void* v, long ldv,
