@@ -1315,8 +1315,10 @@ struct Kv8Plan {
 // us with 8, 61 with 16).  Jobs of 32 queries were no faster than two of 16.
 //
 // Blocks: as many as are resident at once, or one per job where no row has room
-// for more than KV8_WHOLE tokens; those have twice the warps where two an SM are
-// enough (one sequence of 512 tokens and 12 heads: 5.9 us, 6.6 with four warps).
+// for more than KV8_WHOLE tokens and the jobs are not many times the blocks that fit
+// (1536 jobs of up to 512 tokens: 26 us whole, 29 in runs; 4096: 60 and 50; 2048 of
+// up to 64: 23 and 14). Those have twice the warps where two an SM are enough (one
+// sequence of 512 tokens and 12 heads: 5.9 us, 6.6 with four warps).
 static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
   static int sms = 0;
   if (!sms) {
@@ -1333,7 +1335,7 @@ static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
   P.nt = (b.start && b.rows != b.B ? mean > 18 : 10 * ((G + 7) / 8) > 17 * ((G + 15) / 16)) ? 2 : 1;
   const int nq = 8 * P.nt;
   const long jobs = (b.start ? (long)b.rows * G / nq + b.B : (long)b.B * ((G + nq - 1) / nq)) * c.n_kv_heads;
-  const bool whole = (long)b.max_pages * c.page <= KV8_WHOLE;
+  const bool whole = (long)b.max_pages * c.page <= KV8_WHOLE && jobs <= 12L * nsm;
   const int tile = kv8_tile(c.head_dim, P.nt, whole);
   const long tiles = ((long)b.max_pages * c.page + tile - 1) / tile;
   P.fits = jobs * (tiles + KV8_OVER) <= 0x7fffffffL;   // units are counted in 32 bits

@@ -309,10 +309,10 @@ def test_attention_long_at_every_width(torch, kind, dtype, heads, G, d, page, le
     assert s.cache.status() == 0
 
 
-@pytest.mark.parametrize("top,ragged", [(90, False), (90, True), (700, True), (700, False)])
+@pytest.mark.parametrize("top,ragged", [(90, False), (90, True), (700, True), (700, False), (1500, True), (1500, False)])
 def test_many_sequences(torch, top, ragged):
     """More sequences than threads of a block, empty ones and ones without rows
-    among them, for whole jobs (rows of at most 512 tokens) and for runs; also append and read."""
+    among them, for whole jobs (rows of at most 1024 tokens) and for runs; also append and read."""
     rng = np.random.default_rng(top + ragged)
     B, heads, d, P = 300, 2, 32, 16
     lens = [int(n) for n in np.where(rng.random(B) < 0.1, 0, np.exp(rng.uniform(0, np.log(top), B)).astype(int))]
@@ -338,11 +338,11 @@ def test_many_sequences(torch, top, ragged):
     assert np.all(np.abs(v.double().cpu().numpy() - want) <= np.abs(want) * (2.0 ** -11 + 2.0 ** -23) + 2.0 ** -25)
 
 
-@pytest.mark.parametrize("G,d", [(1, 128), (12, 64), (16, 128), (2, 16)])
-def test_many_short_jobs(torch, G, d):
-    """More whole jobs than blocks of eight warps fit at once: blocks of four."""
+@pytest.mark.parametrize("G,d,B", [(1, 128, 160), (12, 64, 160), (16, 128, 160), (2, 16, 160), (1, 32, 1000)])
+def test_many_short_jobs(torch, G, d, B):
+    """More whole jobs than blocks of eight warps fit at once: blocks of four; and
+    so many that the warps take runs of them."""
     rng = np.random.default_rng(d)
-    B = 160
     lens, new = [int(n) for n in rng.integers(0, 120, B)], [1] * B
     s = Setup(torch, "e4m3", 2, d, 32, lens, new, seed=d)
     q, qf = values(torch, s.rng, (B, 2 * G, d), "bf16")

@@ -145,8 +145,8 @@ def test_scratch_is_asked_for_long_rows_only(lib):
         assert lib.gpt_kv8_attention_work(ctypes.byref(cache()), ctypes.byref(batch(max_pages=pages, ld_table=pages, **kw)), 4,
                                           ctypes.byref(n)) == G.GPT_OK
         return n.value
-    assert ask(32) == 0                     # 512 tokens: whole jobs
-    assert 0 < ask(33) <= ask(4000)
+    assert ask(64) == 0                     # 1024 tokens: whole jobs
+    assert 0 < ask(65) <= ask(4000)
     assert ask(4000) <= 64 << 20
     # a multiple that keeps the records behind the sums aligned
     assert ask(4000) % 16 == 0
