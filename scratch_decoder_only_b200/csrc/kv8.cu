@@ -35,7 +35,9 @@ __device__ __forceinline__ bool kv8_unit(const Kv8Seqs& q, int job, int lu, int 
     s.b = job; s.s0 = job; s.n = 1; s.len = q.lens[job];
   }
   if (off == 0 && threadIdx.x == 0 && (s.len < s.n || s.len > cap)) set_dev_err(err, GPT_DEVERR_POS);
-  const int p0 = max(s.len - s.n, 0), p1 = min(s.len, cap);
+  // (a negative length, INT_MIN too, is no token: it must not wrap below)
+  const int p0 = max(max(s.len, 0) - s.n, 0), p1 = min(s.len, cap);
+  if (p1 <= 0) return false;
   u.b = s.b;
   u.unit = (p0 >> lu) + off;
   const int base = u.unit << lu;

@@ -461,6 +461,29 @@ def test_bad_pages_and_lengths(torch):
         assert s.cache.status() & 64
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_lengths_at_the_ends_of_32_bits(torch, kind):
+    """Lengths whose differences with the new tokens pass 32 bits: no token, and the
+    word says so, in each form of each call."""
+    s = Setup(torch, kind, 2, 32, 16, [40, 20], [1, 1], seed=31)
+    before = s.state(torch)
+    for new in ([1, 1], [3, 2]):
+        n = sum(new)
+        x, _ = values(torch, s.rng, (n, 2, 32), "bf16")
+        q, _ = values(torch, s.rng, (n, 4, 32), "bf16")
+        for low in (-2 ** 31, -2 ** 31 + 1, -2 ** 31 + 16, -2 ** 31 + 17, -1, 0):
+            for ragged in (True, False) if new == [1, 1] else (True,):
+                b = s.batch(torch, ragged, lens=[low, low], new=new)
+                s.cache.append(0, x.cuda(), x.cuda(), b)
+                assert s.cache.status() == 16
+                s.cache.read(0, b)
+                assert s.cache.status() == 16
+                out, lse = s.cache.attention(0, q.cuda(), b, return_lse=True)
+                assert torch.all(out == 0) and torch.all(lse == -float("inf")) and s.cache.status() == 16
+    after = s.state(torch)
+    assert all(np.array_equal(a, b) for a, b in zip(before[0] + before[1], after[0] + after[1]))
+
+
 def test_empty_calls(torch):
     s = Setup(torch, "int8", 1, 16, 16, [5], [1], seed=1)
     from scratch_decoder_only_b200.kv8 import KV8Batch
