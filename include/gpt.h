@@ -489,7 +489,8 @@ int gpt_kv8_append(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, co
                    long ldv, int dtype, uint32_t* err, void* stream);
 
 /* The cached keys and values of the sequences' last tokens in 16 bits (code *
- * scale, rounded once): rows as in gpt_kv8_append.  Skipped tokens give 0. */
+ * scale, rounded once): rows as in gpt_kv8_append.  The rows of skipped tokens
+ * are left as they are. */
 int gpt_kv8_read(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, void* k, long ldk, void* v, long ldv,
                  int dtype, uint32_t* err, void* stream);
 

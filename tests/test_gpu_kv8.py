@@ -484,6 +484,34 @@ def test_lengths_at_the_ends_of_32_bits(torch, kind):
     assert all(np.array_equal(a, b) for a, b in zip(before[0] + before[1], after[0] + after[1]))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_read_leaves_rows_of_skipped_tokens(torch, dtype):
+    """Rows outside the starts, of tokens before a sequence's first and of bad pages keep what they hold."""
+    import ctypes
+    from scratch_decoder_only_b200 import gpt as G
+    lens, new, rows = [40, 3, 33], [20, 5, 33], 61
+    s = Setup(torch, "int8", 3, 32, 16, [40, 5, 33], [20, 5, 33], seed=33)
+    table = s.table.copy()
+    table[2, 1] = -7
+    b = s.batch(torch, True, table=table, lens=lens, new=new, rows=rows)
+    out = [torch.full((rows, 96), 7.0, dtype=tdt(torch, dtype), device="cuda") for _ in range(2)]
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert G.load_library().gpt_kv8_read(s.cache._c, 0, b.ref, out[0].data_ptr(), 96, out[1].data_ptr(), 96,
+                                         1 if dtype == "bf16" else 2, s.cache._err, stream) == G.GPT_OK
+    assert s.cache.status() == 16 | 32
+    for w in range(2):
+        want = np.full((rows, 3, 32), 7.0, np.float32)
+        want[0:20] = s.ref.tokens(w, s.table[0], 40)[20:]
+        want[22:25] = s.ref.tokens(w, s.table[1], 3)
+        third = s.ref.tokens(w, s.table[2], 33)
+        want[25:41], want[57:58] = third[:16], third[32:]
+        got = out[w].float().cpu().numpy().reshape(rows, 3, 32)
+        kept = want == 7.0
+        assert np.all(got[kept] == 7.0)
+        # code * scale in fp32, then one rounding (2^-24 and half a step, relative)
+        assert np.all(np.abs(got - want) <= np.abs(want) * (HALF[dtype] + 2.0 ** -23))
+
+
 def test_empty_calls(torch):
     s = Setup(torch, "int8", 1, 16, 16, [5], [1], seed=1)
     from scratch_decoder_only_b200.kv8 import KV8Batch
