@@ -57,8 +57,8 @@ __device__ __forceinline__ int kv8_page(const Kv8Seqs& q, const Kv8Layer& L, int
 
 // ---------------------------------------------------------------------------
 // Append.  A block of 128 threads takes a page of a sequence and a run of heads,
-// keys or values, one head after the other, or four at a time, a warp each, where a
-// page has at most 2048 elements of a head (TPH threads a head).  The next head's
+// keys or values, one head after the other, or four at a time, a warp each (fewer warps
+// for fewer heads), where a page has at most 2048 elements of a head (TPH threads a head).  The next head's
 // rows travel by asynchronous copies into shared memory, each thread's to places
 // of its own, while a head's stay in registers (VPT 16-byte vectors a thread)
 // between their largest magnitude (an unsigned 16-bit maximum over the bit
@@ -133,13 +133,13 @@ template <typename T, int KIND, int VPT, int TPH>
 __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8AppendP p) {
   griddep_wait();
   griddep_release();
-  // the next head's rows, [VPT][128] vectors, each thread's own; value codes [P][D + KV8_PAD]
+  // the next head's rows, [VPT][threads] vectors, each thread's own; value codes [P][D + KV8_PAD]
   extern __shared__ __align__(16) uint8_t ahead[];
   __shared__ unsigned wmax[2][4];
-  constexpr int HEADS = 128 / TPH;   // at a time
+  const int THREADS = TPH == 128 ? 128 : blockDim.x, HEADS = THREADS / TPH;   // heads at a time
   const Kv8Layer& L = p.L;
   const int tid = threadIdx.x % TPH, mate = threadIdx.x / TPH, lp = L.lp, ld = L.ld, D = 1 << ld, row = D + KV8_PAD;
-  uint8_t* turn = ahead + VPT * 128 * 16 + mate * (row << lp);
+  uint8_t* turn = ahead + VPT * THREADS * 16 + mate * (row << lp);
   auto meet = [] {
     if constexpr (TPH == 128) __syncthreads();
     else __syncwarp();
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8Ap
     const uint16_t* y = x + (h << ld);
 #pragma unroll
     for (int j = 0; j < VPT; ++j, y += step)
-      if (j < mine) kv8_copy16(slot + j * 128 * 16, reinterpret_cast<const uint8_t*>(y));
+      if (j < mine) kv8_copy16(slot + j * THREADS * 16, reinterpret_cast<const uint8_t*>(y));
     asm volatile("cp.async.commit_group;" ::: "memory");
     s_next = u.lo > 0 ? scales[h] : 0.f;   // read by all before the barrier, written behind it
   };
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8Ap
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       uint32_t w[4] = {0, 0, 0, 0};
-      if (j < mine) kv8_lds<16>(w, slot + j * 128 * 16);
+      if (j < mine) kv8_lds<16>(w, slot + j * THREADS * 16);
       r[j] = make_uint4(w[0], w[1], w[2], w[3]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) pair = __vmaxu2(pair, w[e] & 0x7fff7fffu);
@@ -1270,15 +1270,18 @@ static int kv8_per_block(int jobs, int n) {
 
 template <typename T, int KIND, int VPT, int TPH>
 static cudaError_t append_v(Kv8AppendP p, const gpt_kv8_cache& c, int jobs, cudaStream_t s) {
-  const size_t smem = (size_t)VPT * 128 * 16 + (size_t)(128 / TPH) * c.page * (c.head_dim + KV8_PAD);
+  // (a warp per head: no more of them than heads; 84653 tokens of one head of 128, pages of 16: 21 us with one warp a
+  // block, 47 with four)
+  const int threads = TPH == 128 ? 128 : 32 * std::min(4, c.n_kv_heads), heads = threads / TPH;
+  const size_t smem = (size_t)VPT * threads * 16 + (size_t)heads * c.page * (c.head_dim + KV8_PAD);
   if (VPT == 16) {   // 50 KB
     const cudaError_t e = cudaFuncSetAttribute(kv8_append_kernel<T, KIND, VPT, TPH>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, 56 * 1024);
     if (e != cudaSuccess) return e;
   }
-  p.heads = kv8_per_block(jobs, (c.n_kv_heads * TPH + 127) / 128) * (128 / TPH);
+  p.heads = kv8_per_block(jobs, (c.n_kv_heads + heads - 1) / heads) * heads;
   const dim3 grid(jobs, (c.n_kv_heads + p.heads - 1) / p.heads, 2);
-  return launch_k(kv8_append_kernel<T, KIND, VPT, TPH>, grid, dim3(128), smem, s, p);
+  return launch_k(kv8_append_kernel<T, KIND, VPT, TPH>, grid, dim3(threads), smem, s, p);
 }
 
 template <typename T, int KIND>

@@ -512,6 +512,31 @@ def test_read_leaves_rows_of_skipped_tokens(torch, dtype):
         assert np.all(np.abs(got - want) <= np.abs(want) * (HALF[dtype] + 2.0 ** -23))
 
 
+@pytest.mark.parametrize("heads,d,page,B", [(1, 16, 16, 1500), (3, 32, 16, 1500), (2, 128, 64, 1100), (1, 16, 16, 18000)])
+def test_append_of_many_sequences(torch, heads, d, page, B):
+    """More sequences than a block has threads, and than their square, some without new tokens."""
+    rng = np.random.default_rng(B + d)
+    new = rng.integers(0, 6, size=B)
+    new[:40] = 0
+    new[-1] = page + 1
+    lens = new + rng.integers(0, 20, size=B)
+    s = Setup(torch, "int8", heads, d, page, lens, new, seed=B)
+    x = [values(torch, rng, (int(new.sum()), heads, d), "bf16") for _ in range(2)]
+    b = s.batch(torch)
+    s.cache.append(0, x[0][0].cuda(), x[1][0].cuda(), b)
+    at = starts(new)
+    for i in range(B):
+        if new[i]:
+            s.ref.append(s.table[i], lens[i], (x[0][1][at[i]:at[i + 1]], x[1][1][at[i]:at[i + 1]]))
+    s.same(torch, lens)
+    got = s.cache.read(0, b)
+    for w in range(2):
+        want = np.concatenate([s.ref.tokens(w, s.table[i], lens[i])[lens[i] - new[i]:] for i in range(B)])
+        # code * scale in fp32 (2^-24), then bf16's half step
+        assert np.all(np.abs(got[w].double().cpu().numpy() - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -23) + 2.0 ** -25)
+    assert s.cache.status() == 0
+
+
 def test_empty_calls(torch):
     s = Setup(torch, "int8", 1, 16, 16, [5], [1], seed=1)
     from scratch_decoder_only_b200.kv8 import KV8Batch
