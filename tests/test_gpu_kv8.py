@@ -338,6 +338,23 @@ def test_many_sequences(torch, top, ragged):
     assert np.all(np.abs(v.double().cpu().numpy() - want) <= np.abs(want) * (2.0 ** -11 + 2.0 ** -23) + 2.0 ** -25)
 
 
+@pytest.mark.parametrize("B,ragged", [(4200, True), (4200, False), (9000, True), (1600, True)])
+def test_attention_of_many_sequences(torch, B, ragged):
+    """A thread's share of the sequences is more than a warp looks at in one step (from 4096 sequences on), or
+    more than one in whole jobs (1600 of one head)."""
+    rng = np.random.default_rng(B)
+    heads, d, P = 1 if B == 1600 else 2, 16, 16
+    lens = [int(n) for n in rng.integers(0, 40, size=B)]
+    lens[B // 3] = 700
+    new = [min(n, int(rng.integers(0, 3))) for n in lens] if ragged else [1] * B
+    if B == 1600:
+        new = [min(n, 1) if i % 20 == 3 else 0 for i, n in enumerate(lens)]
+    s = Setup(torch, "e4m3", heads, d, P, lens, new, seed=4)
+    q, qf = values(torch, s.rng, (sum(new), heads * 3, d), "bf16")
+    out, lse = s.cache.attention(0, q.cuda(), s.batch(torch, ragged), return_lse=True)
+    check(torch, s, qf, out, lse, lens, new, "bf16")
+
+
 @pytest.mark.parametrize("G,d,B", [(1, 128, 160), (12, 64, 160), (16, 128, 160), (2, 16, 160), (1, 32, 1000)])
 def test_many_short_jobs(torch, G, d, B):
     """More whole jobs than blocks of eight warps fit at once: blocks of four; and
