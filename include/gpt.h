@@ -507,8 +507,11 @@ int gpt_kv8_read(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, void
  *  work    device scratch of gpt_kv8_attention_work bytes, 16-byte aligned;
  *          its contents need not survive or be set.  Calls that may run at the
  *          same time need one each.
- * Products are summed in fp32; the softmax weights are rounded to fp16 for
- * their product with the codes.  The same call gives the same bits.
+ * Products are summed in fp32; the softmax weights times their page's value
+ * scale are rounded to fp16 for their product with the codes: by 2^-11 of
+ * themselves where they are at least 2^-28 of the largest such product among the
+ * 32 or 64 tokens beside them (a tile), by 2^-39 of that largest below.  The same
+ * call gives the same bits.
  * Errors: GPT_ERR_ARG (also: n_heads no multiple of n_kv_heads, work_bytes too
  * small, scale not finite), GPT_ERR_CUDA. */
 int gpt_kv8_attention(const gpt_kv8_cache* c, int layer, const gpt_kv8_batch* b, const void* q, long ldq, int n_heads,

@@ -457,8 +457,15 @@ __global__ void __launch_bounds__(128) kv8_read_kernel(Kv8ReadP p) {
 // keeps all of bf16's bits down to 2^-28 of the query's largest element (fp16
 // queries are f16); codes are exact in f16; scores, m, l and the output sum are
 // fp32.  Only the weights lose bits: w * (page's value scale) / (largest value
-// scale so far) is rounded to f16 (2^-12 relative, below the output's own 2^-9
-// or 2^-12), and the output sum is in units of that scale.
+// scale so far) is rounded to f16 (a lone token's 1 stays exact).  Each query's
+// products of a tile are brought by a power of two of their own to a
+// largest of [2^14, 2^15) first, and the tile's sums taken back as they join the
+// output's.  So the rounding is 2^-11 relative down to 2^-28 of the tile's largest
+// product, and 2^-39 of that largest below, whatever the row's other tiles hold:
+// one key far above a long row of small weights, its own value near zero, costs the
+// rest no bits, nor does a page of large values that hardly weighs.  (One unit for
+// the whole row lost both: 17 nats below the row's largest a weight had one bit.)
+// Scales that differ by more than 2^126 leave fp32 on the way.
 //
 // Split: lengths are known on the device only, and a batch may mix a few tokens
 // with a hundred thousand.  So the tiles of all (sequence, NQ queries, head)
@@ -471,13 +478,16 @@ __global__ void __launch_bounds__(128) kv8_read_kernel(Kv8ReadP p) {
 // the tiles in turn, and merges it in shared memory.
 //
 // Measured (one B200, L2 too small for the caches): 64 sequences of 4096 tokens, 8
-// heads of 64, int8: 55 us = 4.9 TB/s of codes (75 % of the copy rate), of which the
-// runs take 48 us (86 %) and the merge 7; one sequence of 131071 tokens, 8 heads
+// heads of 64, int8: 56 us = 4.8 TB/s of codes (73 % of the copy rate), the merge 7
+// of them; one sequence of 131071 tokens, 8 heads
 // of 128, 32 query heads, e4m3: 57 us (72 %); 64 sequences of 0 to 16384 tokens
-// with 1 to 5 rows, 32 query heads of 64: 46 us, bound by the 1.8 passes over each
+// with 1 to 5 rows, 32 query heads of 64: 49 us, bound by the 1.8 passes over each
 // key that 4 to 20 queries take in jobs of 8.  Short rows are bound by the chain
 // length, page, codes, weights, merge: 32 sequences of up to 512 tokens, 12 heads of
-// 64: 10.8 us, one: 5.9.
+// 64: 10.7 us, one: 5.8.  The weights' own powers of two take 0 to 1 us of these, 2.7
+// of the 49 (and 4 of 72 for 64 x 4096 tokens with 16 queries each); skipping them by a
+// vote where all of a tile's weights are large took 48 and 72, a power kept from
+// tile to tile until a maximum leaves a window 48 and 78.
 // ---------------------------------------------------------------------------
 #define KV8_NW 4       // warps of a block that takes runs, or a whole job
 #define KV8_WIDE 8     // of one that takes a whole job where jobs are few
@@ -903,7 +913,7 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
     minlim = min(minlim, __shfl_xor_sync(0xffffffffu, minlim, 1));
     minlim = min(minlim, __shfl_xor_sync(0xffffffffu, minlim, 2));
 
-    float o[NT][KW][4], m[NT][2], l[NT][2], vref = 0.f, vinv = 0.f;
+    float o[NT][KW][4], m[NT][2], l[NT][2], vref = 0.f, vinv = 1.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -950,12 +960,12 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
       fetch_keys();
       advance();
       // ---- weights; a tile that some query sees in part takes the form with comparisons
-      float fac[NT][2];
+      float fac[NT][2], down[NT][2];
       uint32_t wf[TQ / 4][NT][2];
       auto weigh = [&](auto part) {
         constexpr bool PART = decltype(part)::value;
         auto seen = [&](int i, int j, int e) { return !PART || (gk + (c & 1) + 2 * i < lim[j][e] && kon); };
-        bool stale = PART || vs > vref;
+        bool stale = vs > vref && vs <= FLT_MAX;
         float top[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -965,21 +975,19 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
 #pragma unroll
             for (int i = 0; i < TQ / 2; ++i)
               if (seen(i, j, e)) mx = fmaxf(mx, s[i >> 1][j][e + 2 * (i & 1)]);
-            top[j][e] = mx * fac[j][e];   // (-inf * 0 and a NaN scale: NaN, which no maximum takes)
+            top[j][e] = fmaxf(-INFINITY, mx * fac[j][e]);   // (-inf * 0 and a NaN scale: NaN, which no maximum takes)
             stale |= top[j][e] > m[j][e] + 8.f;
           }
         if (__any_sync(0xffffffffu, stale)) {
-          float tv = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 8));
-          tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 16));
-          const float vnew = fmaxf(vref, tv);
-          vinv = vnew > 0.f ? 1.f / vnew : 1.f;   // (all scales 0, or NaN: they stay what they are)
-          const float vold = vnew > 0.f ? vref * vinv : 1.f;
-          vref = vnew;
+          float tv = vs <= FLT_MAX ? vs : 0.f;   // (an infinite scale makes its own rows infinite, no others)
+          tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 8));
+          vref = fmaxf(vref, fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 16)));
+          vinv = 1.f / fmaxf(vref, FLT_MIN);
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(-INFINITY, top[j][e]);
+              float mx = top[j][e];
 #pragma unroll
               for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
               const float mn = fmaxf(m[j][e], mx), al = kv8_ex2(m[j][e] - (mn == -INFINITY ? 0.f : mn));
@@ -987,17 +995,29 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
               l[j][e] *= al;
 #pragma unroll
               for (int i = 0; i < KW; ++i) {
-                o[j][i][e] *= al * vold;
-                o[j][i][e + 2] *= al * vold;
+                o[j][i][e] *= al;
+                o[j][i][e + 2] *= al;
               }
             }
         }
-        const float vfac = vs * vinv;
+        const float vr = vs * vinv;   // at most 1, or infinite or NaN as the scale is
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
+          // the largest product of each column, to a power of two: the upper halves of two fp32 numbers that
+          // are not negative compare as integers (a scale of NaN or nothing seen: 0)
+          uint32_t most[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            most[e] = __float_as_uint(fmaxf(0.f, kv8_ex2(top[j][e] - (m[j][e] == -INFINITY ? 0.f : m[j][e])) * vr));
+          uint32_t both = __vmaxu2(__byte_perm(most[0], most[1], 0x7632), 0x07800780u);   // (2^-112 at least)
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, k));
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float mu = m[j][e] == -INFINITY ? 0.f : m[j][e];
+            const uint32_t p2 = (e ? both : both << 16) & 0x7f800000u;
+            const float vfac = vr * __uint_as_float((268u << 23) - p2);   // 2^14 / p2
+            down[j][e] = vref * __uint_as_float(p2 - (14u << 23));
 #pragma unroll
             for (int i = 0; i < TQ / 2; ++i) {
               float& y = s[i >> 1][j][e + 2 * (i & 1)];
@@ -1038,14 +1058,21 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
             for (int w = 0; w < TQ / 4; ++w) vr[e][w] = von ? kv8_low_bytes(vr[e][w], slen - gv - 4 * w) : 0u;
           }
         }
+        float sum[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sum[j][0] = sum[j][1] = sum[j][2] = sum[j][3] = 0.f;
 #pragma unroll
         for (int i = 0; i < TQ / 4; ++i) {
           uint32_t a[4];
           kv8_widen<KIND>(vr[0][i], a[0], a[2]);
           kv8_widen<KIND>(vr[1][i], a[1], a[3]);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) kv8_mma(o[j][k], a, wf[i][j]);
+          for (int j = 0; j < NT; ++j) kv8_mma(sum[j], a, wf[i][j]);
         }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][k][e] = fmaf(sum[j][e], down[j][e & 1], o[j][k][e]);
       }
     }
 
@@ -1055,11 +1082,6 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], k);
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          o[j][i][e] *= vref;
-          o[j][i][e + 2] *= vref;
-        }
       }
     if constexpr (WHOLE) {
       // ---- merge the warps' queries, each warp's in a buffer of its own
