@@ -30,8 +30,11 @@ struct Kv8PoolP {
   unsigned* err;
 };
 
-// Exclusive sum over the block in thread order; total: of the whole block.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+// Exclusive sum over the block in thread order; total: of the whole block.  Where
+// sums may pass 32 bits, v <= cap <= 2^25 and what matters of a sum is only whether
+// it reaches cap: a warp's sum (below 2^30) counts as cap at most, so the results
+// are below 2^31, right where the true sum is below cap and at least cap elsewhere.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total, int cap = 0x7fffffff) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = v;
 #pragma unroll
@@ -40,7 +43,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
     if (lane >= k) inc += y;
   }
   __syncthreads();   // the sums of an earlier call have been read
-  if (lane == 31) warp_sums[warp] = inc;
+  if (lane == 31) warp_sums[warp] = min(inc, cap);
   __syncthreads();
   int w = warp_sums[lane];
 #pragma unroll
@@ -116,7 +119,9 @@ __global__ void __cluster_dims__(KVP_CTAS, 1, 1) __launch_bounds__(KVP_THREADS)
     __threadfence();
   }
   if (FORK) cl.sync();   // the claims are there
-  // ---- pages that each request needs (an invalid one: none)
+  // ---- pages that each request needs (an invalid one: none); all sums end at one more page than there are, for
+  // rows may ask for 2^27 each
+  const int cap = p.n_pages + 1;
   int carry = 0;
   bool bad_pos = false;
   for (int i0 = 0; i0 < n; i0 += KVP_THREADS) {
@@ -137,17 +142,17 @@ __global__ void __cluster_dims__(KVP_CTAS, 1, 1) __launch_bounds__(KVP_THREADS)
           bad_pos = true;
         } else {
           at = (len + P1) >> p.lp;
-          need = (int)((want + P1) >> p.lp) - at;
+          need = min((int)((want + P1) >> p.lp) - at, cap);
         }
       }
     }
     int tot;
-    const int ex = block_scan(need, wsum, tot);
+    const int ex = block_scan(need, wsum, tot, cap);
     if (i < n) {
-      first[i] = carry + ex;
+      first[i] = min(carry + ex, cap);
       place[i] = at;
     }
-    carry += tot;
+    carry = min(carry + tot, cap);
   }
   if (tid == 0) first[n] = carry;
   if (bad_pos && rank == 0) set_dev_err(p.err, GPT_DEVERR_POS);
@@ -254,9 +259,11 @@ __global__ void __cluster_dims__(KVP_CTAS, 1, 1) __launch_bounds__(KVP_THREADS)
     }
   } else {
     for (int i = tid; i < n; i += KVP_THREADS) {
-      const int ad = add[i], len = p.lens[i], need = first[i + 1] - first[i];
-      if (ad < 0 || len < 0 || (long)len + ad > ((long)p.max_pages << p.lp)) continue;
-      if (need && first[i + 1] > avail) sflag = 1;
+      const int ad = add[i], len = p.lens[i];
+      const long want = (long)len + ad;
+      if (ad < 0 || len < 0 || want > ((long)p.max_pages << p.lp)) continue;
+      // (whether it needs pages the capped sums do not tell)
+      if ((want + P1) >> p.lp > (len + P1) >> p.lp && first[i + 1] > avail) sflag = 1;
       else p.lens[i] = len + ad;
     }
     __syncthreads();
