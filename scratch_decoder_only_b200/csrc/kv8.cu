@@ -1298,11 +1298,27 @@ static Kv8Seqs kv8_seqs(const gpt_kv8_batch& b) {
   return {b.start, b.lens, b.table, b.B, b.max_pages, b.ld_table, b.rows};
 }
 
+int kv8_sms() {
+  static PerDevice known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 148;
+  }
+  const int n = per_device(known, dev, [](int d) {
+    int x = 0;
+    if (cudaDeviceGetAttribute(&x, cudaDevAttrMultiProcessorCount, d) == cudaSuccess) return x;
+    cudaGetLastError();
+    return 0;
+  });
+  return n > 0 ? n : 148;
+}
+
 // Heads (columns of heads) that a block of append or read takes: all of them when
 // there are blocks enough for every SM to hold eight of them even so, fewer for
 // small calls, down to one.
 static int kv8_per_block(int jobs, int n) {
-  const int groups = std::min(n, (148 * 8 * 2 + 2 * jobs - 1) / (2 * jobs));
+  const int groups = std::min(n, (kv8_sms() * 8 * 2 + 2 * jobs - 1) / (2 * jobs));
   return (n + groups - 1) / groups;
 }
 
@@ -1363,17 +1379,8 @@ struct Kv8Plan {
 // up to 64: 23 and 14). Those have twice the warps where two an SM are enough (one
 // sequence of 512 tokens and 12 heads: 5.9 us, 6.6 with four warps).
 static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
-  static int sms = 0;
-  if (!sms) {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess &&
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
-      sms = n;
-    else
-      cudaGetLastError();
-  }
   Kv8Plan P = {};
-  const int G = H / c.n_kv_heads, nsm = sms ? sms : 148;
+  const int G = H / c.n_kv_heads, nsm = kv8_sms();
   const long mean = b.B ? ((long)b.rows * G + b.B - 1) / b.B : G;
   P.nt = (b.start && b.rows != b.B ? mean > 18 : 10 * ((G + 7) / 8) > 17 * ((G + 15) / 16)) ? 2 : 1;
   const int nq = 8 * P.nt;
@@ -1399,16 +1406,16 @@ template <typename T, int D, int NT, int KIND, int NW>
 static cudaError_t attn_launch(const Kv8AttnP& p, const Kv8Plan& P, cudaStream_t s) {
   constexpr size_t smem = kv8_attn_smem<D, NT, NW>();
   if (smem > 40000) {
-    static bool ready[64] = {};   // per device: the attribute is set
+    static PerDevice ready;   // 1: the attribute is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 64 || !ready[dev]) {
+    per_device(ready, dev, [&](int) {
       e = cudaFuncSetAttribute(kv8_attn_kernel<T, D, NT, KIND, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)smem);
-      if (e != cudaSuccess) return e;
-      if (dev < 64) ready[dev] = true;
-    }
+      return e == cudaSuccess ? 1 : 0;
+    });
+    if (e != cudaSuccess) return e;
   }
   ++g_kernel_launches;
   return launch_k(kv8_attn_kernel<T, D, NT, KIND, NW>, dim3(P.blocks), dim3(32 * (NW ? NW : KV8_NW)), smem, s, p);

@@ -3,6 +3,7 @@
 #pragma once
 #include "gpt.h"
 #include "launch.h"
+#include "per_device.h"
 
 // One layer of a cache: codes k [n_pages][Hkv][P][D], v [n_pages][Hkv][P/16][D][16]
 // and one scale per (page, head).
@@ -25,6 +26,8 @@ static inline int ilog2(int x) {
 
 // "" or why the description of a cache cannot be used
 const char* kv8_check_cache(const gpt_kv8_cache* c);
+// SMs of the current device (148, a B200's, where there is none to ask)
+int kv8_sms();
 
 static inline Kv8Layer kv8_layer(const gpt_kv8_cache& c, int layer) {
   Kv8Layer L;

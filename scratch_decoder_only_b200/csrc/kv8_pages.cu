@@ -528,7 +528,7 @@ int gpt_kv8_fork(const gpt_kv8_pool* p, const gpt_kv8_cache* c, const int32_t* s
   if (e != cudaSuccess) return kvp_done("gpt_kv8_fork", e);
   const int chunks = (C.bytes + KVP_CHUNK - 1) / KVP_CHUNK, subs = 2 * C.layers * chunks;
   // two waves of eight blocks an SM: a block looks its pages up once for all that it copies
-  const int share = std::max(1, std::min(subs, 148 * 16 / n));
+  const int share = std::max(1, std::min(subs, kv8_sms() * 16 / n));
   ++g_kernel_launches;
   return kvp_done("gpt_kv8_fork", launch_k(kvp_fork_copy_kernel, dim3((unsigned)share, n), dim3(256), 0, s, P, C, src,
                                            dst, (const int*)done, chunks));
@@ -560,7 +560,7 @@ int gpt_kv8_compact(const gpt_kv8_pool* p, const gpt_kv8_cache* c, int64_t* n_li
   const int chunks = (C.bytes + KVP_CHUNK - 1) / KVP_CHUNK;
   ++g_kernel_launches;
   return kvp_done("gpt_kv8_compact",
-                  launch_k(kvp_move_kernel, dim3(148 * 6), dim3(256), 0, s, P, C, (const int*)work, chunks));
+                  launch_k(kvp_move_kernel, dim3(kv8_sms() * 6), dim3(256), 0, s, P, C, (const int*)work, chunks));
 }
 
 }  // extern "C"

@@ -247,8 +247,10 @@ class KV8Cache(_Calls):
 
     def _work(self, b, H):
         need = ctypes.c_size_t()
-        if self.lib.gpt_kv8_attention_work(self._c, b.ref, H, ctypes.byref(need)) != G.GPT_OK:
-            raise G.GPTError(G.GPT_ERR_ARG, self.lib.gpt_last_error(None).decode())
+        with torch.cuda.device(self._index):   # the scratch depends on the device's SMs
+            rc = self.lib.gpt_kv8_attention_work(self._c, b.ref, H, ctypes.byref(need))
+        if rc != G.GPT_OK:
+            raise G.GPTError(rc, self.lib.gpt_last_error(None).decode())
         return need.value
 
     # -- pages
