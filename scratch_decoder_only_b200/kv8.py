@@ -149,7 +149,9 @@ class KV8Cache(_Calls):
         self._c = ctypes.byref(self.c)
         self.table, self.lens, self.ref, self._pool = table, lens, ref, None
         if ref is not None:
-            if ref.numel() != n or table.device != dev:
+            if table is None or lens is None:
+                raise ValueError("ref needs table and lens beside it")
+            if _i32(ref, "ref", dev).numel() != n or table.device != dev:
                 raise ValueError("ref must have one entry per page, on the GPU that holds k")
             self._pool = KV8Pool(table, lens, ref, p)
             self._pool.err, self._pool._err = self.err, self._err   # one error word for both
@@ -161,6 +163,8 @@ class KV8Cache(_Calls):
         def make(shape, dtype, fill=0):
             return torch.full(shape, fill, dtype=torch.int32, device=device) if dtype == torch.int32 else \
                 torch.zeros(shape, dtype=dtype, device=device)
+        if kind not in _NAMES:
+            raise ValueError("kind must be int8 or e4m3")
         code = _NAMES[kind]
         shape = (n_layers, n_pages, n_kv_heads)
         return cls(make((*shape, page, head_dim), torch.uint8).view(code),

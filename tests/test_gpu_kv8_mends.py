@@ -50,3 +50,15 @@ def test_growth_past_32_bits_of_pages(torch, pages, before, huge, after):
     pool.extend(i32(torch, add))
     assert pool.status() == 0 and int(lens[n]) == free * P and bool((ref == 1).all())
     assert np.array_equal(table[n, :free].cpu().numpy(), np.nonzero(want.ref == 0)[0])
+
+
+def test_a_count_without_its_table_is_refused(torch):
+    """ref alone, or with one of the two that belong to it, is a ValueError like the other bad descriptions."""
+    from scratch_decoder_only_b200.kv8 import KV8Cache
+    c = KV8Cache.empty(1, 8, 2, 64, n_rows=3, max_pages=4)
+    four = (c.k, c.v, c.k_scale, c.v_scale)
+    for more in (dict(ref=c.ref), dict(table=c.table, ref=c.ref), dict(lens=c.lens, ref=c.ref),
+                 dict(table=c.table, lens=c.lens, ref=c.ref.long())):
+        with pytest.raises(ValueError):
+            KV8Cache(*four, **more)
+    assert KV8Cache(*four, c.table, c.lens, c.ref).pool.n_pages == 8

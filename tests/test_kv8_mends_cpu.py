@@ -48,3 +48,9 @@ def test_numbers_are_kept_for_each_device(tmp_path):
     subprocess.run([cxx, "-std=c++17", "-Wall", "-Werror", "-pthread", "-I",
                     os.path.join(ROOT, "scratch_decoder_only_b200", "csrc"), str(src), "-o", str(exe)], check=True)
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_an_unknown_kind_is_refused():
+    from scratch_decoder_only_b200.kv8 import KV8Cache
+    with pytest.raises(ValueError):
+        KV8Cache.empty(1, 8, 2, 64, kind="fp8", device="cpu")
