@@ -285,11 +285,12 @@ int gpt_beam_decode(gpt_model* m, const int32_t* prompt, int B, int Tp, int n_ne
  *  prompt    device int32 [B, Tp]
  *  uniforms  device float [B, n_samples, n_new], values in [0, 1)
  *  out       device int32 [B, n_samples, n_new]
- * The first call allocates the cache (2 * n_layers * max_batch * max_seq *
- * n_kv_heads * head size bytes and a few), which gpt_destroy frees; it must
- * come before any stream capture.
+ * The first call allocates the cache (2 * n_layers * min(max_batch, 32) *
+ * max_seq * n_kv_heads * head size bytes and a few), which gpt_destroy frees,
+ * beside the 16-bit one that gpt_create made; it must come before any stream
+ * capture.
  * Requires 16-bit precision, vocab <= 55000, B * n_samples <= max_batch and
- * <= 32, Tp + n_new - 1 <= max_seq.
+ * <= 32, Tp + n_new - 1 <= max_seq, min(max_batch, 32) * max_seq <= 2^28.
  * Errors: as gpt_sample_decode; GPT_ERR_NOMEM. */
 int gpt_sample_parallel(gpt_model* m, const int32_t* prompt, int B, int Tp, int n_new, int n_samples, int kv_kind,
                         const gpt_sampling* sp, const float* uniforms, int32_t* out);

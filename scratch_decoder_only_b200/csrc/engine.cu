@@ -1033,8 +1033,12 @@ static DecLayout dec_layout(const gpt_model* m) {
   } while (0)
 
 #define KV8_PAGE 16   // tokens a page: a fork copies half of one on average
+#define KV8_ROWS 32   // rows a call has at most
 
-// Device int arrays of the paged decode, for R = max_batch rows.
+// Rows of the paged decode's cache and arrays.
+static int kv8_rows(const gpt_model* m) { return std::min(m->Bmax, KV8_ROWS); }
+
+// Device int arrays of the paged decode, for R rows.
 struct Kv8Arrays {
   int *prompt_add, *one, *prompt_lens, *start, *src, *dst, *rows, *done;
   size_t n;
@@ -1042,7 +1046,7 @@ struct Kv8Arrays {
 static Kv8Arrays kv8_arrays(const gpt_model* m) {
   Kv8Arrays a;
   int* p = m->kv8_ints;
-  const int R = m->Bmax;
+  const int R = kv8_rows(m);
   a.prompt_add = p; p += R;
   a.one = p; p += R;
   a.prompt_lens = p; p += R;
@@ -1057,8 +1061,8 @@ static Kv8Arrays kv8_arrays(const gpt_model* m) {
 
 static int kv8_alloc(gpt_model* m) {
   if (m->kv8_buf) return GPT_OK;
-  const int R = m->Bmax, mp = (m->Tmax + KV8_PAGE - 1) / KV8_PAGE;
-  if ((long)R * mp > (1L << 24) || R > 16384) FAIL(GPT_ERR_ARG, "max_batch * max_seq too large for the paged cache");
+  const int R = kv8_rows(m), mp = (m->Tmax + KV8_PAGE - 1) / KV8_PAGE;
+  if ((long)R * mp > (1L << 24)) FAIL(GPT_ERR_ARG, "min(max_batch, 32) * max_seq too large for the paged cache");
   gpt_kv8_cache c = {};
   c.n_layers = m->NL; c.n_pages = R * mp; c.n_kv_heads = m->Hkv; c.head_dim = m->d; c.page = KV8_PAGE;
   gpt_kv8_pool p = {};
@@ -1099,7 +1103,7 @@ static int kv8_alloc(gpt_model* m) {
 template <typename T>
 static int kv8_fill(gpt_model* m, int B, int Tp, cudaStream_t s) {
   Acts<T> A(m);
-  const int n = m->kv8_n, R = m->Bmax;
+  const int n = m->kv8_n, R = kv8_rows(m);
   const gpt_kv8_pool& P = m->kv8_pool;
   const Kv8Arrays a = kv8_arrays(m);
   std::vector<int> h(a.n);
@@ -1684,7 +1688,7 @@ int gpt_sample_parallel(gpt_model* m, const int32_t* prompt, int B, int Tp, int 
   if (!(sp->temperature >= 0.f) || sp->top_k < 0 || !(sp->top_p > 0.f && sp->top_p <= 1.f))
     FAIL(GPT_ERR_ARG, "need temperature >= 0, top_k >= 0, 0 < top_p <= 1");
   if (m->V > SMP_MAX_VOCAB) FAIL(GPT_ERR_ARG, "vocabulary too large for the sampling kernel");
-  if (B < 1 || n_samples < 1 || (long)B * n_samples > m->Bmax || (long)B * n_samples > 32)
+  if (B < 1 || n_samples < 1 || (long)B * n_samples > kv8_rows(m))
     FAIL(GPT_ERR_ARG, "B * n_samples out of range [1, min(max_batch, 32)]");
   if (Tp < 1 || n_new < 1) FAIL(GPT_ERR_ARG, "Tp and n_new must be >= 1");
   if ((long)Tp + n_new - 1 > m->Tmax) FAIL(GPT_ERR_STATE, "Tp + n_new - 1 exceeds max_seq");
