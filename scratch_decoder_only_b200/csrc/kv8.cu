@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(128, VPT <= 8 ? 5 : 3) kv8_append_kernel(Kv8Ap
 // One new token per sequence (no starts), as every decode step has: a warp per
 // (sequence, head, keys | values), lanes over channels, no barrier.  Three
 // dependent loads (length, page, then the token, its page's scale and the values'
-// 16-token group together) are all there is: 2.4 us where the block form above
+// 16-token group together) are all there is: 3.1 us where the block form above
 // takes 4.7 (32 sequences, 12 heads of 64).
 template <typename T, int KIND, int D>
 __global__ void __launch_bounds__(128) kv8_append_one_kernel(Kv8AppendP p) {
@@ -1365,19 +1365,23 @@ struct Kv8Plan {
   bool fits;
   size_t part, ml, piece;  // floats (piece: in floats too)
 };
-// Queries a job: 16 where that saves enough passes over the cache.  A pass with
-// 16 queries costs 1.7 of one with 8 (64 x 4096 tokens in L2: 12 warps an SM
-// instead of 16, and 1.3 times the instructions), so they are taken for 9 to 16
-// queries a sequence (70 against 90 us for 16 of 64 channels) and 25 to 32; where the
+// Queries a job: 16 where that saves enough passes over the cache (12 warps an SM
+// instead of 16, and more instructions a pass).  64 x 4096 tokens, 8 heads of 64, us
+// with 8 and with 16: 8 queries a sequence 58 and 73, 9 to 16 92 and 73, 17 to 24 128
+// and 128, 25 to 32 178 and 129, so 9 to 16 and 25 to 32 take 16.  Where the
 // sequences' rows differ, only their mean is known here, and half a job is lost
-// a sequence on average: from 19 on (mean 12, one to five rows of four heads: 48
-// us with 8, 61 with 16).  Jobs of 32 queries were no faster than two of 16.
+// a sequence on average: 64 x 3000 tokens, means of 8, 12, 14, 16, 18, 22, 34: 55, 70,
+// 76, 80, 93, 99, 132 with 8 and 63, 74, 81, 81, 87, 95, 124 with 16, so 16 from 19 on.
+// Jobs of 32 queries were no faster than two of 16.
 //
 // Blocks: as many as are resident at once, or one per job where no row has room
-// for more than KV8_WHOLE tokens and the jobs are not many times the blocks that fit
-// (1536 jobs of up to 512 tokens: 26 us whole, 29 in runs; 4096: 60 and 50; 2048 of
-// up to 64: 23 and 14). Those have twice the warps where two an SM are enough (one
-// sequence of 512 tokens and 12 heads: 5.9 us, 6.6 with four warps).
+// for more than KV8_WHOLE tokens and the jobs are not many times the blocks that fit.
+// Heads of 64, us whole and in runs: 300 jobs of 64, 256, 1024 tokens 5.5, 6.9, 16 and
+// 8.6, 16, 22; 1200 jobs 13, 18, 39 and 11, 23, 46; 1700 jobs 14, 21, 46 and 12, 23, 56;
+// 3000 jobs 25, 34, 79 and 18, 35, 82, with lengths spread below those 32, 33, 45 and
+// 22, 26, 38.  (Rows of up to 64 tokens would be better in runs from about 900 jobs on;
+// the bound is the longer rows'.)  Whole jobs have twice the warps where two blocks an
+// SM are enough (one sequence of 512 tokens and 12 heads: 5.9 us, 6.6 with four warps).
 static Kv8Plan kv8_plan(const gpt_kv8_cache& c, const gpt_kv8_batch& b, int H) {
   Kv8Plan P = {};
   const int G = H / c.n_kv_heads, nsm = kv8_sms();
