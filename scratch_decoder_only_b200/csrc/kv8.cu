@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(128) kv8_read_kernel(Kv8ReadP p) {
 // scale so far) is rounded to f16 (a lone token's 1 stays exact).  Each query's
 // products of a tile are brought by a power of two of their own to a
 // largest of [2^14, 2^15) first, and the tile's sums taken back as they join the
-// output's.  So the rounding is 2^-11 relative down to 2^-28 of the tile's largest
+// output's, which are in units of that scale.  So the rounding is 2^-11 relative down to 2^-28 of the tile's largest
 // product, and 2^-39 of that largest below, whatever the row's other tiles hold:
 // one key far above a long row of small weights, its own value near zero, costs the
 // rest no bits, nor does a page of large values that hardly weighs.  (One unit for
@@ -979,10 +979,11 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
             stale |= top[j][e] > m[j][e] + 8.f;
           }
         if (__any_sync(0xffffffffu, stale)) {
-          float tv = vs <= FLT_MAX ? vs : 0.f;   // (an infinite scale makes its own rows infinite, no others)
+          const float vwas = vref;
+          float tv = vs <= FLT_MAX ? fmaxf(vs, FLT_MIN) : FLT_MIN;   // (an infinite scale makes its own rows infinite, no others)
           tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 8));
           vref = fmaxf(vref, fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 16)));
-          vinv = 1.f / fmaxf(vref, FLT_MIN);
+          vinv = 1.f / vref;
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -995,8 +996,8 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
               l[j][e] *= al;
 #pragma unroll
               for (int i = 0; i < KW; ++i) {
-                o[j][i][e] *= al;
-                o[j][i][e + 2] *= al;
+                o[j][i][e] *= al * (vwas * vinv);
+                o[j][i][e + 2] *= al * (vwas * vinv);
               }
             }
         }
@@ -1017,7 +1018,7 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
             const float mu = m[j][e] == -INFINITY ? 0.f : m[j][e];
             const uint32_t p2 = (e ? both : both << 16) & 0x7f800000u;
             const float vfac = vr * __uint_as_float((268u << 23) - p2);   // 2^14 / p2
-            down[j][e] = vref * __uint_as_float(p2 - (14u << 23));
+            down[j][e] = __uint_as_float(p2 - (14u << 23));
 #pragma unroll
             for (int i = 0; i < TQ / 2; ++i) {
               float& y = s[i >> 1][j][e + 2 * (i & 1)];
@@ -1082,6 +1083,11 @@ __global__ void __launch_bounds__(32 * (NW ? NW : KV8_NW), kv8_resident(D, NT, N
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], k);
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          o[j][i][e] *= vref;
+          o[j][i][e + 2] *= vref;
+        }
       }
     if constexpr (WHOLE) {
       // ---- merge the warps' queries, each warp's in a buffer of its own

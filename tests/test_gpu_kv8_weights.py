@@ -162,6 +162,23 @@ def test_scales_that_leave_fp32(torch, kind, dtype, d, page, G, L, above, nats):
     assert s.cache.status() == 0
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,page,G,L", [(64, 16, 1, 70), (128, 16, 12, 300), (32, 64, 4, 2000)])
+@pytest.mark.parametrize("scale", [2.0 ** -126, 2.0 ** -120, 2.0 ** 100, 0.0])
+def test_scales_at_the_ends_of_fp32(torch, kind, d, page, G, L, scale):
+    """Values of 1e-36, of 1e31, and none: one rounding to bf16 like any others."""
+    s = Setup(torch, kind, 1, d, page, [L], [1], seed=L)
+    rng = np.random.default_rng(L)
+    vs = np.full_like(s.ref.s[1], scale)
+    vs[rng.random(vs.shape) < 0.5] *= 1.5
+    put(torch, s, vs=vs)
+    q = (2.0 * torch.randn(1, G, d, generator=torch.Generator().manual_seed(2))).to(torch.bfloat16)
+    out = s.cache.attention(0, q.cuda(), s.batch(torch, False))
+    for h in range(G):
+        near(s, 0, q[0, h].double().numpy(), out[0, h], L, 0, "bf16", d ** -0.5)
+    assert s.cache.status() == 0
+
+
 @pytest.mark.parametrize("kind,dtype,d,L", [("int8", "fp16", 64, 64), ("e4m3", "bf16", 128, 200), ("int8", "bf16", 32, 1500)])
 @pytest.mark.parametrize("last", [2.0 ** 25, float("nan"), float("inf"), 0.0])
 def test_pages_that_later_rows_see(torch, kind, dtype, d, L, last):
