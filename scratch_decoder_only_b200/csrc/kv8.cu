@@ -481,11 +481,11 @@ __global__ void __launch_bounds__(128) kv8_read_kernel(Kv8ReadP p) {
 // heads of 64, int8: 56 us = 4.8 TB/s of codes (73 % of the copy rate), the merge 7
 // of them; one sequence of 131071 tokens, 8 heads
 // of 128, 32 query heads, e4m3: 57 us (72 %); 64 sequences of 0 to 16384 tokens
-// with 1 to 5 rows, 32 query heads of 64: 49 us, bound by the 1.8 passes over each
+// with 1 to 5 rows, 32 query heads of 64: 48.5 us, bound by the 1.8 passes over each
 // key that 4 to 20 queries take in jobs of 8.  Short rows are bound by the chain
 // length, page, codes, weights, merge: 32 sequences of up to 512 tokens, 12 heads of
-// 64: 10.7 us, one: 5.8.  The weights' own powers of two take 0 to 1 us of these, 2.7
-// of the 49 (and 4 of 72 for 64 x 4096 tokens with 16 queries each); skipping them by a
+// 64: 10.7 us, one: 5.8.  The weights' own powers of two take 0 to 1 us of these, 2.3
+// of the 48.5 (and 4 of 72 for 64 x 4096 tokens with 16 queries each); skipping them by a
 // vote where all of a tile's weights are large took 48 and 72, a power kept from
 // tile to tile until a maximum leaves a window 48 and 78.
 // ---------------------------------------------------------------------------
